@@ -64,7 +64,9 @@ typedef enum {
 #define MILO_DEV_TIMEOUT 0x8        /* a bounded pipeline wait gave up; outputs invalid */
 /* Checked build only (libmilo_checked.so, compiled with MILO_CHECKED): an
  * index or copy range fell outside its buffer; that access was skipped and
- * the outputs are invalid.  The normal build performs no such checks. */
+ * the outputs are invalid.  The normal build performs no such checks, except
+ * that milo_dispatch, milo_combine and their gradients check every inv_perm
+ * entry in both builds (one outside -1..T*k-1 counts as dropped). */
 #define MILO_DEV_BOUNDS 0x10
 
 /* Router flags. */
@@ -322,6 +324,126 @@ MILO_API milo_status milo_route(const uint16_t* logits, int32_t T, int32_t E, in
                        uint32_t flags, int32_t* topk_ids, float* topk_w,
                        int32_t* expert_offsets, int32_t* perm, int32_t* inv_perm,
                        int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Token rows in expert order                                               */
+/* ------------------------------------------------------------------------ */
+/*
+ * The move of token rows into expert order and back as calls of their own, for
+ * expert products that run outside milo_moe_forward (milo_grouped_linear over
+ * grouped rows, experts kept in 16 bits, training before quantisation), with
+ * their gradients.  f = t*k + j is the flat slot of token t's j-th pick and
+ * p = inv_perm[f] its row in expert order (milo_route's inv_perm; -1: the slot
+ * was dropped; every other entry in 0..T*k-1, no two alike):
+ *     dispatch            xs[p] = w[f] x[t]
+ *     combine             y[t]  = r[t] + sum_j w[f] ys[p]
+ *     dispatch_backward   dx[t] = sum_j w[f] dxs[p],   dw[f] = <dxs[p], x[t]>
+ *     combine_backward    dys[p] = w[f] dy[t],         dw[f] = <dy[t], ys[p]>
+ * (the gradient of r is dy itself).  Sums run in fp32 in slot order and are
+ * rounded once to the output's type.
+ *   Token rows are [T, H], expert rows [T*k, H], row-major, F16, BF16 or F32;
+ *   the inputs of one call share a type, the output (and combine's r) has its
+ *   own.  Any H from 1 to 2^24; rows of H % 8 == 0 at 16-byte aligned
+ *   addresses move in 16-byte pieces, others element by element.
+ *   w   f32 [T*k] (milo_route's topk_w), or NULL: 1.
+ *   dw  f32 [T*k], 0 for a dropped slot; or NULL: not wanted (ys or x may then
+ *       be NULL).  With dw, w and ys / x are required.
+ * Expert rows that no slot points to -- those behind the last expert's when
+ * slots were dropped -- are neither read nor written.  A token whose slots are
+ * all dropped gets r (or 0).  y may be r's own buffer; no other output may
+ * overlap an input.
+ * Errors: INVALID_ARG (bad T, H or dtype, NULL or misaligned pointers, dw
+ * without w or its rows), UNSUPPORTED_SHAPE (k outside 1..16, H above 2^24,
+ * T*k above MILO_MAX_ROWS, T*H above 2^38).  Device: BOUNDS (an inv_perm entry
+ * outside its range; it counts as dropped), FP16_RANGE (an fp16 output
+ * overflows).  dev_status may be NULL.  T = 0 does nothing.  Stream-ordered.
+ */
+MILO_API milo_status milo_dispatch(const void* x, milo_dtype x_dt, int32_t T, int32_t k, int32_t H,
+                                   const int32_t* inv_perm, const float* w, void* xs, milo_dtype xs_dt,
+                                   int32_t* dev_status, void* stream);
+MILO_API milo_status milo_combine(const void* ys, milo_dtype ys_dt, int32_t T, int32_t k, int32_t H,
+                                  const int32_t* inv_perm, const float* w, const void* residual, void* y,
+                                  milo_dtype y_dt, int32_t* dev_status, void* stream);
+MILO_API milo_status milo_dispatch_backward(const void* dxs, milo_dtype dxs_dt, int32_t T, int32_t k, int32_t H,
+                                            const int32_t* inv_perm, const float* w, const void* x, void* dx,
+                                            milo_dtype dx_dt, float* dw, int32_t* dev_status, void* stream);
+MILO_API milo_status milo_combine_backward(const void* dy, milo_dtype dy_dt, int32_t T, int32_t k, int32_t H,
+                                           const int32_t* inv_perm, const float* w, const void* ys, void* dys,
+                                           milo_dtype dys_dt, float* dw, int32_t* dev_status, void* stream);
+
+/*
+ * milo_route_backward -- gradient of milo_route's weights with respect to the
+ * logits.  With s = sum_j w_j dw_j over a token's picks e_j:
+ *     MILO_ROUTE_RENORM:  dl[e_j] = w_j (dw_j - s), 0 for the other experts
+ *     otherwise:          dl[e] = [e = e_j] w_j dw_j - softmax(l)_e s
+ *   logits    fp16 [T, E], as given to milo_route (may be NULL with RENORM)
+ *   topk_ids, topk_w   [T, k], as milo_route wrote them; dw f32 [T, k]
+ *   flags     0 or MILO_ROUTE_RENORM, as given to milo_route
+ *   dlogits   [T, E] in dl_dt (F16, BF16 or F32), every element written
+ * Limits as milo_route.  Errors: INVALID_ARG (T < 0, unknown flag or dtype,
+ * NULL pointers), UNSUPPORTED_SHAPE.  Device: BAD_EXPERT_ID (an id outside
+ * [0, E): that pick contributes nothing), NONFINITE (NaN/Inf logits; NaN
+ * counts as -inf), FP16_RANGE.  dev_status may be NULL.  Stream-ordered.
+ */
+MILO_API milo_status milo_route_backward(const uint16_t* logits, const int32_t* topk_ids, const float* topk_w,
+                                         const float* dw, int32_t T, int32_t E, int32_t k, uint32_t flags,
+                                         void* dlogits, milo_dtype dl_dt, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Dense 16-bit projections                                                 */
+/* ------------------------------------------------------------------------ */
+/*
+ * The projections around the quantised experts that stay in 16 bits -- the
+ * router's own product, attention projections, shared experts -- and their
+ * gradients.  x [M, K] and W [N, K] are row-major in the same type dt, F16 or
+ * BF16; products are exact, sums fp32.  Any M and N; K a multiple of 8; M, N
+ * and K at most 2^24, M*N, M*K and N*K at most 2^38.
+ */
+#define MILO_ACT_NONE 0
+#define MILO_ACT_RELU 1       /* max(z, 0) */
+#define MILO_ACT_SILU 2       /* z / (1 + exp(-z)) */
+#define MILO_ACT_GELU 3       /* z (1 + erf(z / sqrt 2)) / 2 */
+#define MILO_ACT_GELU_TANH 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+
+/*
+ * milo_dense_linear -- z = x W^T + bias;  y = act(z) + residual, in one kernel.
+ *   bias      [N] in dt, or NULL
+ *   residual  [M, N] in y_dt, or NULL; may be y's own buffer
+ *   y         [M, N] in y_dt (F16, BF16 or F32), rounded once from fp32
+ *   z         NULL, or [M, N] in dt: the pre-activation, which
+ *             milo_dense_linear_backward needs when there is an activation
+ * x and W 16-byte aligned, the others aligned to their elements; y and z
+ * overlap no input but residual.  M = 0 does nothing.
+ * Errors: INVALID_ARG (M < 0, N or K < 1, unknown dtype or act, NULL or
+ * misaligned pointers), UNSUPPORTED_SHAPE (K % 8, sizes above the limits),
+ * CUDA.  Device: FP16_RANGE (an fp16 y or z overflows), TIMEOUT.  dev_status
+ * may be NULL.  Stream-ordered; no workspace.
+ */
+MILO_API milo_status milo_dense_linear(const void* x, const void* W, milo_dtype dt, int32_t M, int32_t N, int32_t K,
+                                       const void* bias, const void* residual, int32_t act, void* y,
+                                       milo_dtype y_dt, void* z, int32_t* dev_status, void* stream);
+
+/*
+ * milo_dense_linear_backward -- with dz = dy act'(z):
+ *     dx = dz W [M, K],   dW = dz^T x [N, K],   db = sum over the rows of dz [N]
+ * each in dt, or NULL: not wanted (the gradient of residual is dy itself).
+ *   dy   [M, N] in dy_dt (F16, BF16 or F32)
+ *   z    [M, N] in dt as milo_dense_linear wrote it; may be NULL for
+ *        MILO_ACT_NONE.  relu'(0) = 0.
+ * dz enters the products rounded to dt, as any 16-bit gradient does (exact
+ * when there is no activation and dy_dt = dt); db sums it in fp32 unrounded.
+ *   ws   milo_dense_linear_backward_workspace_bytes, 256-byte aligned
+ * x, W, dx and dW 16-byte aligned, the others aligned to their elements.
+ * x may be NULL without dW, W without dx.  M = 0 writes zeros to dW and db.
+ * Errors: as milo_dense_linear, and WORKSPACE.  Device: FP16_RANGE (dz or a
+ * gradient overflows fp16), TIMEOUT.  dev_status may be NULL.  Stream-ordered,
+ * deterministic.
+ */
+MILO_API milo_status milo_dense_linear_backward_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* bytes);
+MILO_API milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_dt, const void* x, const void* W,
+                                                milo_dtype dt, int32_t M, int32_t N, int32_t K, int32_t act,
+                                                const void* z, void* dx, void* dW, void* db, void* ws,
+                                                size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Quantised projections and layers                                         */

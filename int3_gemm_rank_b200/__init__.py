@@ -30,6 +30,7 @@ MILO_LORC_F16, MILO_LORC_INT3 = 0, 1
 MILO_DEV_BAD_EXPERT_ID, MILO_DEV_NONFINITE, MILO_DEV_FP16_RANGE, MILO_DEV_TIMEOUT, MILO_DEV_BOUNDS = 1, 2, 4, 8, 16
 MILO_ROUTE_RENORM, MILO_ROUTE_IDS_GIVEN = 1, 2
 MILO_GEMM_AUTO, MILO_GEMM_MMA, MILO_GEMM_TC = 0, 1, 2
+MILO_ACT_NONE, MILO_ACT_RELU, MILO_ACT_SILU, MILO_ACT_GELU, MILO_ACT_GELU_TANH = range(5)
 MILO_GROUP, MILO_MAX_RANK = 64, 64
 
 # The C ABI symbols of include/milo.h (checked by the tests).
@@ -39,7 +40,10 @@ EXPORTS = ("milo_status_str", "milo_last_error", "milo_version", "milo_pack", "m
            "milo_moe_forward", "milo_moe_h_offset", "milo_set_profile_events",
            "milo_grouped_linear_noalloc", "milo_packed_bytes", "milo_hqq_pack",
            "milo_quantize_lorc_workspace", "milo_quantize_lorc", "milo_kurtosis_workspace", "milo_kurtosis",
-           "milo_assign_ranks", "milo_selftest_wait_timeout", "milo_set_gemm_path", "milo_dequantize")
+           "milo_assign_ranks", "milo_selftest_wait_timeout", "milo_set_gemm_path", "milo_dequantize",
+           "milo_dispatch", "milo_combine", "milo_dispatch_backward", "milo_combine_backward",
+           "milo_route_backward", "milo_dense_linear", "milo_dense_linear_backward_workspace_bytes",
+           "milo_dense_linear_backward")
 
 
 class MiloError(RuntimeError):
@@ -133,6 +137,21 @@ def lib() -> C.CDLL:
         L.milo_selftest_wait_timeout.argtypes = [vp, vp]; L.milo_selftest_wait_timeout.restype = C.c_int
         L.milo_set_gemm_path.argtypes = [i32]; L.milo_set_gemm_path.restype = C.c_int
         L.milo_dequantize.argtypes = [vp, i32, i32, vp, vp]; L.milo_dequantize.restype = C.c_int
+        for name in ("milo_dispatch", "milo_combine", "milo_dispatch_backward", "milo_combine_backward"):
+            getattr(L, name).restype = C.c_int
+        L.milo_dispatch.argtypes = [vp, C.c_int, i32, i32, i32, vp, vp, vp, C.c_int, vp, vp]
+        L.milo_combine.argtypes = [vp, C.c_int, i32, i32, i32, vp, vp, vp, vp, C.c_int, vp, vp]
+        L.milo_dispatch_backward.argtypes = [vp, C.c_int, i32, i32, i32, vp, vp, vp, vp, C.c_int, vp, vp, vp]
+        L.milo_combine_backward.argtypes = [vp, C.c_int, i32, i32, i32, vp, vp, vp, vp, C.c_int, vp, vp, vp]
+        L.milo_route_backward.argtypes = [vp, vp, vp, vp, i32, i32, i32, u32, vp, C.c_int, vp, vp]
+        L.milo_route_backward.restype = C.c_int
+        L.milo_dense_linear.argtypes = [vp, vp, C.c_int, i32, i32, i32, vp, vp, i32, vp, C.c_int, vp, vp, vp]
+        L.milo_dense_linear.restype = C.c_int
+        L.milo_dense_linear_backward_workspace_bytes.argtypes = [i32, i32, i32, C.POINTER(sz)]
+        L.milo_dense_linear_backward_workspace_bytes.restype = C.c_int
+        L.milo_dense_linear_backward.argtypes = [vp, C.c_int, vp, vp, C.c_int, i32, i32, i32, i32, vp, vp, vp, vp,
+                                                 vp, sz, vp, vp]
+        L.milo_dense_linear_backward.restype = C.c_int
         _lib = L
     return _lib
 
@@ -465,6 +484,258 @@ def milo_route(logits: torch.Tensor | None, k: int, renorm: bool, E: int | None 
         _check(lib().milo_route(_ptr(logits), T, E, k, flags, _ptr(ids), _ptr(w), _ptr(off), _ptr(perm),
                                 _ptr(inv), _ptr(dev_status), _stream()), "milo_route")
     return {"ids": ids, "w": w, "offsets": off, "perm": perm[:T * k], "inv_perm": inv[:T * k]}
+
+
+def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, logits: torch.Tensor | None = None,
+                        out_dtype=torch.float16, dlogits: torch.Tensor | None = None,
+                        dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient [T, E] of milo_route's softmax weights with respect to the
+    logits, from dw f32 [T, k] (as milo_combine_backward returns it).  `route`
+    is the dict milo_route returned for fp16 `logits` [T, E] with the same
+    `renorm`; a renormalised gradient does not need the logits."""
+    ids, w = route["ids"], route["w"]
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("route['ids'] must be [T, k]")
+    dev = ids.device
+    T, k = ids.shape
+    _arg(ids, "route['ids']", (torch.int32,))
+    _arg(w, "route['w']", (torch.float32,), shape=(T, k), device=dev)
+    _arg(dw, "dw", (torch.float32,), shape=(T, k), device=dev)
+    if logits is not None:
+        _arg(logits, "logits", (torch.float16,), shape=(T, E), device=dev)
+    elif not renorm:
+        raise ValueError("milo_route_backward: logits are required without renorm")
+    dlogits = _out(dlogits, "dlogits", (T, E), out_dtype, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_route_backward", _ptr(logits), _ptr(ids), _ptr(w), _ptr(dw), T, E, k,
+            MILO_ROUTE_RENORM if renorm else 0, _ptr(dlogits), _dt(dlogits), _ptr(dev_status))
+    return dlogits
+
+
+# ---------------------------------------------------------------------------
+# token rows in expert order
+# ---------------------------------------------------------------------------
+
+def _launch(dev, name: str, *args):
+    """Call a stream-ordered entry point on the current stream of `dev`."""
+    if dev.index == torch.cuda.current_device():
+        status = getattr(lib(), name)(*args, _stream())
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, _stream())
+    if status != MILO_OK:
+        _check(status, name)
+
+
+def _out(t, name: str, shape: tuple, dtype, device):
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        if dtype not in _OUT:
+            raise ValueError(f"{name} must be {' or '.join(_dname(d) for d in _OUT)}, not {_dname(dtype)}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    _arg(t, name, _OUT, shape=shape, device=device)
+    return t
+
+
+def _slots(route: dict, what: str) -> tuple:
+    """T, k and the inverse permutation of a route dict (milo_route's `ids`
+    [T, k] and `inv_perm` [T*k])."""
+    ids, inv = route["ids"], route["inv_perm"]
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError(f"{what}: route['ids'] must be [T, k]")
+    T, k = ids.shape
+    _arg(inv, "route['inv_perm']", (torch.int32,), min_numel=T * k)
+    return T, k, inv
+
+
+def _rows(t, name: str, rows: int, H: int | None, dtype, dev) -> int:
+    """Checks rows [rows, H] on `dev` (any H and type when not given); returns H."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+    if t.dim() != 2 or t.shape[0] != rows or (H is not None and t.shape[1] != H):
+        raise ValueError(f"{name} must be [{rows}, {'H' if H is None else H}], not {tuple(t.shape)}")
+    _arg(t, name, _OUT if dtype is None else (dtype,), device=dev)
+    return t.shape[1]
+
+
+def _weights(w, T: int, k: int, dev):
+    if w is not None:
+        _arg(w, "w", (torch.float32,), shape=(T, k), device=dev)
+
+
+def milo_dispatch(x: torch.Tensor, route: dict, w: torch.Tensor | None = None, out_dtype=None,
+                  xs: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """Token rows x [T, H] into expert order: xs [T*k, H] with xs[inv_perm[f]] =
+    w[f] * x[f // k] (w f32 [T, k], or None: 1).  Rows behind the last expert's
+    (dropped slots) stay as the buffer holds them."""
+    T, k, inv = _slots(route, "milo_dispatch")
+    dev = inv.device
+    H = _rows(x, "x", T, None, None, dev)
+    _weights(w, T, k, dev)
+    xs = _out(xs, "xs", (T * k, H), out_dtype or x.dtype, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_dispatch", _ptr(x), _dt(x), T, k, H, _ptr(inv), _ptr(w), _ptr(xs), _dt(xs), _ptr(dev_status))
+    return xs
+
+
+def milo_combine(ys: torch.Tensor, route: dict, w: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                 out_dtype=None, y: torch.Tensor | None = None,
+                 dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """Expert rows ys [T*k, H] back to token order: y[t] = residual[t] +
+    sum_j w[t, j] * ys[inv_perm[t*k + j]] (w f32 [T, k], usually route["w"], or
+    None: 1; the residual in y's type, which may be y itself)."""
+    T, k, inv = _slots(route, "milo_combine")
+    dev = inv.device
+    H = _rows(ys, "ys", T * k, None, None, dev)
+    _weights(w, T, k, dev)
+    if residual is not None and y is None and out_dtype is None:
+        out_dtype = residual.dtype
+    y = _out(y, "y", (T, H), out_dtype or ys.dtype, dev)
+    if residual is not None:
+        _rows(residual, "residual", T, H, y.dtype, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_combine", _ptr(ys), _dt(ys), T, k, H, _ptr(inv), _ptr(w), _ptr(residual), _ptr(y), _dt(y),
+            _ptr(dev_status))
+    return y
+
+
+def milo_dispatch_backward(dxs: torch.Tensor, route: dict, x: torch.Tensor | None = None,
+                           w: torch.Tensor | None = None, out_dtype=None, dx: torch.Tensor | None = None,
+                           dw: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> tuple:
+    """Gradients (dx [T, H], dw f32 [T, k]) of milo_dispatch from dxs [T*k, H];
+    dw is None when the call had no weights (x is needed only for dw)."""
+    T, k, inv = _slots(route, "milo_dispatch_backward")
+    dev = inv.device
+    H = _rows(dxs, "dxs", T * k, None, None, dev)
+    _weights(w, T, k, dev)
+    if w is not None and x is not None:
+        _rows(x, "x", T, H, dxs.dtype, dev)
+        dw = _grad_w(dw, T, k, dev)
+    elif dw is not None:
+        raise ValueError("milo_dispatch_backward: dw needs the call's w and x")
+    dx = _out(dx, "dx", (T, H), out_dtype or dxs.dtype, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_dispatch_backward", _ptr(dxs), _dt(dxs), T, k, H, _ptr(inv), _ptr(w),
+            None if dw is None else _ptr(x), _ptr(dx), _dt(dx), _ptr(dw), _ptr(dev_status))
+    return dx, dw
+
+
+def milo_combine_backward(dy: torch.Tensor, route: dict, ys: torch.Tensor | None = None,
+                          w: torch.Tensor | None = None, out_dtype=None, dys: torch.Tensor | None = None,
+                          dw: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> tuple:
+    """Gradients (dys [T*k, H], dw f32 [T, k]) of milo_combine from dy [T, H];
+    dw is None when the call had no weights (ys is needed only for dw).  The
+    residual's gradient is dy.  Rows of dys behind the last expert's (dropped
+    slots) stay as the buffer holds them."""
+    T, k, inv = _slots(route, "milo_combine_backward")
+    dev = inv.device
+    H = _rows(dy, "dy", T, None, None, dev)
+    _weights(w, T, k, dev)
+    if w is not None and ys is not None:
+        _rows(ys, "ys", T * k, H, dy.dtype, dev)
+        dw = _grad_w(dw, T, k, dev)
+    elif dw is not None:
+        raise ValueError("milo_combine_backward: dw needs the call's w and ys")
+    dys = _out(dys, "dys", (T * k, H), out_dtype or dy.dtype, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_combine_backward", _ptr(dy), _dt(dy), T, k, H, _ptr(inv), _ptr(w),
+            None if dw is None else _ptr(ys), _ptr(dys), _dt(dys), _ptr(dw), _ptr(dev_status))
+    return dys, dw
+
+
+def _grad_w(dw, T: int, k: int, dev):
+    if dw is None:
+        return torch.empty((T, k), dtype=torch.float32, device=dev)
+    _arg(dw, "dw", (torch.float32,), shape=(T, k), device=dev)
+    return dw
+
+
+# ---------------------------------------------------------------------------
+# dense 16-bit projections
+# ---------------------------------------------------------------------------
+
+_ACTS = {"none": MILO_ACT_NONE, "relu": MILO_ACT_RELU, "silu": MILO_ACT_SILU, "gelu": MILO_ACT_GELU,
+         "gelu_tanh": MILO_ACT_GELU_TANH}
+
+
+def _dense_args(x, W, act: str) -> tuple:
+    """Checks x [M, K] and W [N, K] (one 16-bit type); returns M, N, K, the
+    device and the activation's code."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a [N, K] tensor")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"x must be [M, {W.shape[1]}]")
+    _arg(x, "x", _ACT)
+    _arg(W, "W", (x.dtype,), device=x.device)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, not {act!r}")
+    return x.shape[0], W.shape[0], x.shape[1], x.device, _ACTS[act]
+
+
+def milo_dense_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                      residual: torch.Tensor | None = None, out_dtype=None, z: torch.Tensor | None = None,
+                      y: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """y = act(x W^T + bias) + residual for x [M, K], W [N, K] in fp16 or bf16
+    (bias [N] in the same type, the residual [M, N] in y's type, which may be y
+    itself).  act: none, relu, silu, gelu or gelu_tanh.  `z`, a [M, N] tensor
+    of x's type, receives the pre-activation x W^T + bias for
+    milo_dense_linear_backward."""
+    M, N, K, dev, a = _dense_args(x, W, act)
+    if bias is not None:
+        _arg(bias, "bias", (x.dtype,), shape=(N,), device=dev)
+    if residual is not None and y is None and out_dtype is None:
+        out_dtype = residual.dtype
+    y = _out(y, "y", (M, N), out_dtype or x.dtype, dev)
+    if residual is not None:
+        _arg(residual, "residual", (y.dtype,), shape=(M, N), device=dev)
+    if z is not None:
+        _arg(z, "z", (x.dtype,), shape=(M, N), device=dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_dense_linear", _ptr(x), _ptr(W), _dt(x), M, N, K, _ptr(bias), _ptr(residual), a, _ptr(y),
+            _dt(y), _ptr(z), _ptr(dev_status))
+    return y
+
+
+def milo_dense_linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    nb = C.c_size_t()
+    _check(lib().milo_dense_linear_backward_workspace_bytes(M, N, K, C.byref(nb)),
+           "milo_dense_linear_backward_workspace_bytes")
+    return nb.value
+
+
+def milo_dense_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "none",
+                               z: torch.Tensor | None = None, need=("dx", "dW", "db"), out: dict | None = None,
+                               ws: torch.Tensor | None = None, dev_status: torch.Tensor | None = None) -> dict:
+    """Gradients of milo_dense_linear from dy [M, N]: a dict of those named in
+    `need` -- dx [M, K], dW [N, K], db [N], in x's type.  `z` is what the
+    forward call kept (required with an activation); the residual's gradient is
+    dy.  `out` may hold buffers for the gradients, `ws` a workspace of
+    milo_dense_linear_backward_workspace_bytes."""
+    M, N, K, dev, a = _dense_args(x, W, act)
+    _arg(dy, "dy", _OUT, shape=(M, N), device=dev)
+    if z is not None:
+        _arg(z, "z", (x.dtype,), shape=(M, N), device=dev)
+    elif a != MILO_ACT_NONE:
+        raise ValueError("milo_dense_linear_backward: z is required with an activation")
+    shapes = {"dx": (M, K), "dW": (N, K), "db": (N,)}
+    grads = {}
+    for name in need:
+        if name not in shapes:
+            raise ValueError(f"need holds {name!r}; it may hold dx, dW and db")
+        t = out.get(name) if out else None
+        if t is None:
+            t = torch.empty(shapes[name], dtype=x.dtype, device=dev)
+        else:
+            _arg(t, name, (x.dtype,), shape=shapes[name], device=dev)
+        grads[name] = t
+    if ws is None:
+        ws = torch.empty(milo_dense_linear_backward_workspace_bytes(M, N, K) + 256, dtype=torch.uint8, device=dev)
+    wp, wn = _ws_arg(ws, dev)
+    _status_arg(dev_status, dev)
+    _launch(dev, "milo_dense_linear_backward", _ptr(dy), _dt(dy), _ptr(x), _ptr(W), _dt(x), M, N, K, a, _ptr(z),
+            _ptr(grads.get("dx")), _ptr(grads.get("dW")), _ptr(grads.get("db")), C.c_void_p(wp), wn,
+            _ptr(dev_status))
+    return grads
 
 
 # ---------------------------------------------------------------------------
