@@ -54,10 +54,9 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 2-D row-major tensor [rows, cols] with row pitch `pitch` bytes; box {bcols, brows}.
-static milo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols,
-                            uint64_t rows, uint64_t pitch, uint32_t bcols, uint32_t brows, const char* what,
-                            CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE) {
+// (declared in milo_host.h)
+milo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+                     uint64_t pitch, uint32_t bcols, uint32_t brows, const char* what, CUtensorMapSwizzle swz) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MILO_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     cuuint64_t dims[2] = {cols, rows};

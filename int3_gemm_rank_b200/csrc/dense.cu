@@ -21,62 +21,6 @@
 namespace milo {
 
 // ---------------------------------------------------------------------------
-// product: 64 x 64 tiles on the CUDA cores, fp32
-// ---------------------------------------------------------------------------
-constexpr int kSgTile = 64, kSgK = 16;
-
-__global__ void __launch_bounds__(256) dense_simple_kernel(const DenseGemm g) {
-    __shared__ float as[kSgK][kSgTile + 4], bs[kSgK][kSgTile + 4];
-    grid_dep_launch();
-    grid_dep_wait();
-    const int tq = (g.Q + kSgTile - 1) / kSgTile;
-    const int p0 = static_cast<int>(blockIdx.x / tq) * kSgTile, q0 = static_cast<int>(blockIdx.x % tq) * kSgTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    int32_t st = 0;
-    for (int c0 = 0; c0 < g.C; c0 += kSgK) {
-        for (int i = threadIdx.x; i < kSgK * kSgTile; i += 256) {
-            {
-                const int r = g.a_mn ? i % kSgTile : i / kSgK, c = g.a_mn ? i / kSgTile : i % kSgK;
-                const bool in = p0 + r < g.P && c0 + c < g.C;
-                as[c][r] = in ? load16(g.a, g.a_mn ? (c0 + c) * g.lda + p0 + r : (p0 + r) * g.lda + c0 + c, g.bf16) : 0.f;
-            }
-            {
-                const int r = g.b_mn ? i % kSgTile : i / kSgK, c = g.b_mn ? i / kSgTile : i % kSgK;
-                const bool in = q0 + r < g.Q && c0 + c < g.C;
-                bs[c][r] = in ? load16(g.b, g.b_mn ? (c0 + c) * g.ldb + q0 + r : (q0 + r) * g.ldb + c0 + c, g.bf16) : 0.f;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kSgK; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[c][4 * ty + i], bs[c][4 * tx + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int p = p0 + 4 * ty + i, q = q0 + 4 * tx + j;
-            if (p >= g.P || q >= g.Q) continue;
-            const size_t o = static_cast<size_t>(p) * g.Q + q;
-            float v = acc[i][j];
-            if (g.bias) v += load16(g.bias, q, g.bf16);
-            if (g.z) static_cast<uint16_t*>(g.z)[o] = round16(v, g.bf16, st);
-            v = dense_act(g.act, v);
-            if (g.residual) v += load_any(g.residual, o, g.y_dt);
-            store_any(g.y, o, g.y_dt, v, st);
-        }
-    flag(g.dev_status, st);
-}
-
-milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
-    const long long tiles = static_cast<long long>((g.P + kSgTile - 1) / kSgTile) * ((g.Q + kSgTile - 1) / kSgTile);
-    return check_cuda(launch_pdl(dense_simple_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, g), what);
-}
-
-// ---------------------------------------------------------------------------
 // dz = dy act'(z), and its column sums
 // ---------------------------------------------------------------------------
 constexpr int kDzRows = 64;         // rows of a block

@@ -1,0 +1,573 @@
+// dense_tc.cu -- the dense 16-bit product D[p, q] = sum_c A(p, c) B(q, c) on the
+// 5th-generation tensor cores (tcgen05, TMEM), with bias, activation and
+// residual in its epilogue (see dense.cu for the three products it serves).
+//
+// Design (B200):
+//   - A work item is a 128 x BN tile of D.  One warp brings 64-deep slices of A
+//     and B by 2-D TMA (128-byte swizzle) into a ring of stages, one warp
+//     issues tcgen05.mma (M = 128, N = BN, K = 16, fp32 accumulator in TMEM),
+//     four warps turn the finished accumulator into output.
+//   - Either operand may lie along c (K-major: a box of 64 c by 128 rows) or
+//     along its rows (MN-major: boxes of 64 rows by 64 c); only the boxes'
+//     coordinates and the matrix descriptors differ, so W and x are read as
+//     they are stored by the forward product and by both gradients.
+//   - Many tiles: a persistent grid, two accumulators in TMEM, so that the
+//     epilogue of one tile runs under the products of the next.
+//   - Few tiles: c is split over the CTAs of a cluster.  Each leaves its
+//     partial tile in its shared memory; after a cluster barrier every warp
+//     of the cluster takes a share of the tile and adds the partials in rank
+//     order (no workspace, no atomics, the same bits every time).
+//   - Few tokens: the operands change places (SWAP), the weight's rows fill
+//     the 128 rows of the tile and the tokens its BN columns, so one token
+//     costs a tile of 16 columns, not of 128 rows.
+//   - Ragged edges need no care in the loads (TMA fills zeros) and are cut in
+//     the epilogue's stores.
+//   - Every wait is bounded: on a timeout the kernel flags MILO_DEV_TIMEOUT,
+//     waits for its copies and products and frees TMEM before it leaves.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "milo_dense.cuh"
+#include "milo_host.h"
+#include "milo_tc.cuh"
+
+namespace milo {
+
+constexpr int kDtRows = 128;                 // rows of A in a tile (MMA M)
+constexpr int kDtK = 64;                     // c per stage: one 128-byte swizzled row
+constexpr int kDtAtom = kDtRows * kDtK * 2;  // bytes of an A stage
+constexpr int kDtBox = 64 * kDtK * 2;        // bytes of an MN-major box (64 rows x 64 c)
+constexpr int kDtThreads = 192;              // producer, MMA, four epilogue warps
+constexpr int kDtMaxStages = 12;
+constexpr int kDtMaxSplit = 8;               // portable cluster size
+constexpr int kDtPitch = 144;                // bytes between rows of the output staging (32 fp32, padded)
+constexpr int kDtStaging = 32 * kDtPitch;    // per epilogue warp
+constexpr int kDtBias = 256;                 // fp32 bias columns, per epilogue warp
+constexpr int kDtChunk = 32;                 // accumulator columns handled at a time
+
+struct DenseTc {
+    CUtensorMap a_map, b_map;
+    int P, Q, C;
+    int a_mn, b_mn, bf16;
+    int bn, stages, split, kblocks;          // columns of a tile; c slices of 64
+    int tiles_p, tiles_q, tiles;
+    uint32_t idesc, tmem_cols;
+    int bufs;                                // accumulators in TMEM (2: persistent)
+    int stage_bytes, off_staging, off_bias, off_bar;
+    int vec;                                 // 16-byte output rows
+    // epilogue (y, residual and z are [M, N]; SWAP: p is the feature)
+    const void *bias, *residual;
+    void *y, *z;
+    int act, y_dt;
+    int32_t* dev_status;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at the same shared-memory address of CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_peer(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Matrix descriptor of an MN-major operand in the 128-byte swizzled layout:
+// rows of 64 elements along MN, 8-c groups 1024 bytes apart, blocks of 64
+// elements along MN one box apart.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(kDtBox >> 4) << 16;           // leading byte offset: next 64 rows
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;             // stride byte offset: next 8 c
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// Item order: bands of kDtBand row tiles, columns inside a band, the band's
+// row tiles fastest, so that the CTAs at work share operand tiles in L2.
+constexpr int kDtBand = 16;
+__device__ __forceinline__ void dense_tile(const DenseTc& p, int item, int& tp, int& tq) {
+    const int per = kDtBand * p.tiles_q;
+    const int band = item / per, in = item - band * per;
+    const int h = min(kDtBand, p.tiles_p - band * kDtBand);
+    tq = in / h;
+    tp = band * kDtBand + in - tq * h;
+}
+
+// ---------------------------------------------------------------------------
+// epilogue of 32 rows (lane = row p) by 32 columns q0.. of D, normal form:
+// y[p, q].  v holds the lane's row.  st32 is the warp's staging buffer.
+// ---------------------------------------------------------------------------
+
+// The warp's 32 x 32 block between staging rows (kDtPitch apart) and global
+// rows p0.., columns q0..; E bytes an element.  16-byte pieces when p.vec.
+template <int E, bool LOAD>
+__device__ __forceinline__ void dense_block(const DenseTc& p, void* g, uint8_t* stg, int p0, int q0, int lane) {
+    constexpr int kPieces = 32 * E / 16;              // 16-byte pieces of a row
+    constexpr int kRows = 32 / kPieces;               // rows of one pass
+    if (p.vec) {
+        const int piece = lane % kPieces, r0 = lane / kPieces;
+        const bool in = q0 + piece * (16 / E) < p.Q;  // Q is a multiple of a piece here
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+            const int r = r0 + i * kRows;
+            if (in && p0 + r < p.P) {
+                uint4* gp = reinterpret_cast<uint4*>(static_cast<uint8_t*>(g) +
+                                                     (static_cast<size_t>(p0 + r) * p.Q + q0) * E) + piece;
+                uint4* sp = reinterpret_cast<uint4*>(stg + r * kDtPitch) + piece;
+                if constexpr (LOAD) *sp = *gp;
+                else *gp = *sp;
+            }
+        }
+    } else {
+        using T = typename std::conditional<E == 4, uint32_t, uint16_t>::type;
+        if (q0 + lane < p.Q)
+            for (int r = 0; r < 32 && p0 + r < p.P; ++r) {
+                T* gp = static_cast<T*>(g) + static_cast<size_t>(p0 + r) * p.Q + q0 + lane;
+                T* sp = reinterpret_cast<T*>(stg + r * kDtPitch) + lane;
+                if constexpr (LOAD) *sp = *gp;
+                else *gp = *sp;
+            }
+    }
+}
+
+// The lane's staging row <-> 32 values, as fp32 (F32) or 16-bit.
+__device__ __forceinline__ void stage_put(uint8_t* row, const float (&v)[32], int dt, int32_t& st) {
+    if (dt == MILO_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w[q] = static_cast<uint32_t>(round16(v[8 * i + 2 * q], dt == MILO_BF16, st)) |
+                       (static_cast<uint32_t>(round16(v[8 * i + 2 * q + 1], dt == MILO_BF16, st)) << 16);
+            reinterpret_cast<uint4*>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[32], uint8_t* stg, const float* bias,
+                                                  int p0, int q0, int lane, int32_t& st) {
+    uint8_t* row = stg + lane * kDtPitch;
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += bias[i];
+    }
+    if (p.z) {
+        stage_put(row, v, p.bf16 ? MILO_BF16 : MILO_F16, st);
+        __syncwarp();
+        dense_block<2, false>(p, p.z, stg, p0, q0, lane);
+        __syncwarp();
+    }
+    if (p.act != MILO_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = dense_act(p.act, v[i]);
+    }
+    if (p.residual) {
+        if (p.y_dt == MILO_F32) dense_block<4, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
+        else dense_block<2, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
+        __syncwarp();
+        if (p.y_dt == MILO_F32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += reinterpret_cast<const float*>(row)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += act_f32(reinterpret_cast<const uint16_t*>(row)[i], p.y_dt == MILO_BF16);
+        }
+        __syncwarp();
+    }
+    stage_put(row, v, p.y_dt, st);
+    __syncwarp();
+    if (p.y_dt == MILO_F32) dense_block<4, false>(p, p.y, stg, p0, q0, lane);
+    else dense_block<2, false>(p, p.y, stg, p0, q0, lane);
+    __syncwarp();
+}
+
+// Swapped form: the lane's row is feature p0 + lane, its N values tokens q0..:
+// y[q, p], consecutive lanes at consecutive addresses.
+template <int N>
+__device__ __forceinline__ void dense_store_swapped(const DenseTc& p, const float (&v)[N], int p0, int q0, int lane,
+                                                    int32_t& st) {
+    const int f = p0 + lane;
+    if (f >= p.P) return;
+    const float b = p.bias ? load16(p.bias, f, p.bf16) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (q0 + i >= p.Q) break;
+        const size_t o = static_cast<size_t>(q0 + i) * p.P + f;
+        float t = v[i] + b;
+        if (p.z) static_cast<uint16_t*>(p.z)[o] = round16(t, p.bf16, st);
+        t = dense_act(p.act, t);
+        if (p.residual) t += load_any(p.residual, o, p.y_dt);
+        store_any(p.y, o, p.y_dt, t, st);
+    }
+}
+
+template <bool SWAP>
+__global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(const __grid_constant__ DenseTc p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
+    uint64_t* empty = full + kDtMaxStages;
+    uint64_t* afull = empty + kDtMaxStages;      // accumulator finished
+    uint64_t* aempty = afull + 2;                // accumulator read
+    uint64_t* done_bar = aempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.split > 1 ? cluster_rank() : 0u;
+
+    grid_dep_launch();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&afull[b], 1);
+            mbar_init(&aempty[b], 4);
+        }
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+    }
+    // TMEM only once the kernels before have left: a CTA that held columns while
+    // it waits for them could keep one of their CTAs from its own
+    grid_dep_wait();
+    if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+
+    // this CTA's share of c (all of it without a split)
+    const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * rank / p.split);
+    const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / p.split);
+    const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
+    int32_t st_bits = 0;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        int stage = 0;
+        uint32_t phase = 0, filled = 0, fph = 0;
+        bool fail = false;
+        const uint32_t tx = kDtAtom + p.bn * 128;
+        for (int it = first; it < p.tiles && !fail; it += step) {
+            int tp, tq;
+            dense_tile(p, it, tp, tq);
+            const int p0 = tp * kDtRows, q0 = tq * p.bn;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait(&empty[stage], phase ^ 1)) {
+                    fail = true;
+                    break;
+                }
+                uint8_t* sa = smem + stage * p.stage_bytes;
+                uint8_t* sb = sa + kDtAtom;
+                uint64_t* fb = &full[stage];
+                filled |= 1u << stage;
+                fph = (fph & ~(1u << stage)) | (phase << stage);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(fb, tx);
+                    if (p.a_mn) {
+                        tma_load_2d(sa, &p.a_map, fb, p0, kb * kDtK);
+                        tma_load_2d(sa + kDtBox, &p.a_map, fb, p0 + 64, kb * kDtK);
+                    } else {
+                        tma_load_2d(sa, &p.a_map, fb, kb * kDtK, p0);
+                    }
+                    if (p.b_mn) {
+                        for (int j = 0; j < p.bn / 64; ++j)
+                            tma_load_2d(sb + j * kDtBox, &p.b_map, fb, q0 + 64 * j, kb * kDtK);
+                    } else {
+                        tma_load_2d(sb, &p.b_map, fb, kb * kDtK, q0);
+                    }
+                }
+                __syncwarp();
+                if (++stage == p.stages) { stage = 0; phase ^= 1; }
+            }
+        }
+        // no copy may still be landing in shared memory when the CTA leaves
+        for (int s = 0; s < p.stages; ++s)
+            if (((filled >> s) & 1u) && !warp_wait(&full[s], (fph >> s) & 1u)) fail = true;
+        if (fail) st_bits |= MILO_DEV_TIMEOUT;
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bph = 0;
+        bool fail = false;
+        const uint64_t astep = p.a_mn ? 128u : 2u, bstep = p.b_mn ? 128u : 2u;   // 16 c further, in 16-byte units
+        for (int it = first; it < p.tiles && !fail; it += step) {
+            if (!warp_wait(&aempty[buf], bph ^ 1)) {
+                fail = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tbase + static_cast<uint32_t>(buf * p.bn);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait(&full[stage], phase)) {
+                    fail = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + kDtAtom;
+                const uint64_t da = p.a_mn ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
+                const uint64_t db = p.b_mn ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
+#pragma unroll
+                for (int q = 0; q < kDtK / 16; ++q)
+                    tc_mma_ss(d, da + q * astep, db + q * bstep, p.idesc, kb > kb0 || q > 0 ? 1u : 0u);
+                tc_commit(&empty[stage]);
+                if (++stage == p.stages) { stage = 0; phase ^= 1; }
+            }
+            tc_commit(&afull[buf]);
+            if (++buf == p.bufs) { buf = 0; bph ^= 1; }
+        }
+        if (fail) st_bits |= MILO_DEV_TIMEOUT;
+        // every issued MMA has completed before TMEM is released
+        tc_commit(done_bar);
+        if (!warp_wait(done_bar, 0)) st_bits |= MILO_DEV_TIMEOUT;
+    } else if (p.split == 1) {
+        // ---------------------------------------------------------------- epilogue, whole tiles
+        const int quarter = warp & 3;
+        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
+        uint8_t* stg = smem + p.off_staging + quarter * kDtStaging;
+        float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + quarter * kDtBias;   // the warp's own copy
+        int buf = 0;
+        uint32_t bph = 0;
+        for (int it = first; it < p.tiles; it += step) {
+            int tp, tq;
+            dense_tile(p, it, tp, tq);
+            const int p0 = tp * kDtRows + 32 * quarter, q0 = tq * p.bn;
+            if constexpr (!SWAP) {
+                if (p.bias) {
+                    for (int i = lane; i < p.bn; i += 32)
+                        sbias[i] = q0 + i < p.Q ? load16(p.bias, q0 + i, p.bf16) : 0.0f;
+                    __syncwarp();
+                }
+            }
+            if (!warp_wait(&afull[buf], bph)) {
+                st_bits |= MILO_DEV_TIMEOUT;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = lane_base + static_cast<uint32_t>(buf * p.bn);
+            if constexpr (SWAP) {
+                for (int c = 0; c < p.bn; c += 16) {
+                    uint32_t d[16];
+                    tc_ld(acc + c, d);
+                    tc_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]);
+                    dense_store_swapped(p, v, p0, q0 + c, lane, st_bits);
+                }
+            } else {
+                for (int c = 0; c < p.bn; c += kDtChunk) {
+                    uint32_t d[32];
+                    tc_ld(acc + c, d);
+                    tc_wait_ld();
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+                    if (p0 < p.P && q0 + c < p.Q) dense_store_chunk(p, v, stg, sbias + c, p0, q0 + c, lane, st_bits);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aempty[buf]);
+            if (++buf == p.bufs) { buf = 0; bph ^= 1; }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue, split over the cluster:
+        // this CTA's partial tile to its shared memory (the stages are done
+        // with: the accumulator's commit covers every MMA that read them)
+        const int quarter = warp & 3;
+        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
+        float* part = reinterpret_cast<float*>(smem);
+        if (!warp_wait(&afull[0], 0)) st_bits |= MILO_DEV_TIMEOUT;
+        tc_fence_after();
+        for (int c = 0; c < p.bn; c += 16) {
+            uint32_t d[16];
+            tc_ld(lane_base + c, d);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * kDtRows + 32 * quarter + lane] = __uint_as_float(d[i]);
+        }
+        tc_fence_before();
+    }
+
+    if (p.split > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2) {
+            // units of 32 rows by 16 (SWAP) or 32 columns, over the cluster's epilogue warps
+            int tp, tq;
+            dense_tile(p, first, tp, tq);
+            constexpr int W = SWAP ? 16 : kDtChunk;
+            const int quarter = warp & 3;
+            uint8_t* stg = smem + p.off_staging + quarter * kDtStaging;
+            float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + quarter * kDtBias;
+            const uint32_t base = smem_u32(smem);
+            const int units = 4 * (p.bn / W);
+            for (int u = static_cast<int>(rank) * 4 + quarter; u < units; u += p.split * 4) {
+                const int r0 = 32 * (u & 3), c0 = W * (u >> 2);
+                const int p0 = tp * kDtRows + r0, q0 = tq * p.bn + c0;
+                if (p0 >= p.P || q0 >= p.Q) continue;
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] = 0.0f;
+                for (int s = 0; s < p.split; ++s)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) v[i] += ld_peer(base + ((c0 + i) * kDtRows + r0 + lane) * 4, s);
+                if constexpr (SWAP) {
+                    dense_store_swapped(p, v, p0, q0, lane, st_bits);
+                } else {
+                    if (p.bias) {
+                        sbias[lane] = q0 + lane < p.Q ? load16(p.bias, q0 + lane, p.bf16) : 0.0f;
+                        __syncwarp();
+                    }
+                    dense_store_chunk(p, v, stg, sbias, p0, q0, lane, st_bits);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();      // no CTA leaves while another still reads its partial tile
+    }
+    flag(p.dev_status, st_bits);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, p.tmem_cols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+constexpr int kDtSmemMax = 227 * 1024 - 1024;     // less the slack that aligns the base
+
+static int dense_sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+// Instruction descriptor: D f32, A and B both fp16 or both bf16, each K- or
+// MN-major, M = 128, N = bn.
+static uint32_t dense_idesc(int bf16, int a_mn, int b_mn, int bn) {
+    const uint32_t t = bf16 ? 1u : 0u;
+    return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kDtRows >> 4) << 24);
+}
+
+template <bool SWAP>
+static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStream_t s) {
+    static std::atomic<bool> configured[64];     // set once per device (a repeat is harmless)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(dense_tc_kernel<SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtSmemMax + 1024);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kDtThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP>, p);
+}
+
+milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
+    DenseTc p;
+    memset(&p, 0, sizeof(p));
+    // few rows of A (tokens): they become the columns
+    const bool swap = g.P <= 128 && !g.a_mn;
+    p.P = swap ? g.Q : g.P;
+    p.Q = swap ? g.P : g.Q;
+    p.C = g.C;
+    p.a_mn = swap ? g.b_mn : g.a_mn;
+    p.b_mn = swap ? g.a_mn : g.b_mn;
+    const void* a = swap ? g.b : g.a;
+    const void* b = swap ? g.a : g.b;
+    const long long lda = swap ? g.ldb : g.lda, ldb = swap ? g.lda : g.ldb;
+    p.bf16 = g.bf16;
+    p.kblocks = (p.C + kDtK - 1) / kDtK;
+    p.tiles_p = (p.P + kDtRows - 1) / kDtRows;
+    const int sms = dense_sms();
+    if (swap) {
+        p.bn = static_cast<int>(round_up(p.Q, 16));
+    } else {
+        p.bn = 256;
+        while (p.bn > 64 && (p.bn / 2 >= p.Q ||
+                             static_cast<long long>(p.tiles_p) * ((p.Q + p.bn - 1) / p.bn) < sms))
+            p.bn /= 2;
+    }
+    p.tiles_q = (p.Q + p.bn - 1) / p.bn;
+    const long long tiles = static_cast<long long>(p.tiles_p) * p.tiles_q;
+    if (tiles > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
+    p.tiles = static_cast<int>(tiles);
+    p.split = 1;
+    while (p.split < kDtMaxSplit && p.tiles * p.split * 2 <= 2 * sms && p.kblocks >= 4 * p.split) p.split *= 2;
+    p.bufs = p.split == 1 && p.tiles > sms ? 2 : 1;
+    p.stage_bytes = kDtAtom + p.bn * 128;
+    const int extra = 4 * kDtStaging + 4 * kDtBias * 4 + 512;
+    const int kper = (p.kblocks + p.split - 1) / p.split;
+    p.stages = std::min({kDtMaxStages, (kDtSmemMax - extra) / p.stage_bytes, std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
+    int ring = p.stages * p.stage_bytes;
+    if (p.split > 1) ring = std::max(ring, p.bn * kDtRows * 4);
+    p.off_staging = ring;
+    p.off_bias = p.off_staging + 4 * kDtStaging;
+    p.off_bar = p.off_bias + 4 * kDtBias * 4;
+    const int smem = p.off_bar + 512 + 1024;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < static_cast<uint32_t>(p.bufs * p.bn)) p.tmem_cols *= 2;
+    p.idesc = dense_idesc(p.bf16, p.a_mn, p.b_mn, p.bn);
+    p.bias = g.bias;
+    p.residual = g.residual;
+    p.y = g.y;
+    p.z = g.z;
+    p.act = g.act;
+    p.y_dt = g.y_dt;
+    p.dev_status = g.dev_status;
+    p.vec = g.Q % 8 == 0 && aligned(g.y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
+
+    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    milo_status st;
+    // K-major [rows, c]: box 64 c by the tile's rows; MN-major [c, rows]: box 64 rows by 64 c
+    st = p.a_mn ? make_map(&p.a_map, a, dt, p.P, p.C, lda * 2, 64, kDtK, what, CU_TENSOR_MAP_SWIZZLE_128B)
+                : make_map(&p.a_map, a, dt, p.C, p.P, lda * 2, kDtK, kDtRows, what, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != MILO_OK) return st;
+    st = p.b_mn ? make_map(&p.b_map, b, dt, p.Q, p.C, ldb * 2, 64, kDtK, what, CU_TENSOR_MAP_SWIZZLE_128B)
+                : make_map(&p.b_map, b, dt, p.C, p.Q, ldb * 2, kDtK, p.bn, what, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != MILO_OK) return st;
+    const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
+    return check_cuda(swap ? launch_dense_tc<true>(p, grid, smem, s) : launch_dense_tc<false>(p, grid, smem, s), what);
+}
+
+}  // namespace milo

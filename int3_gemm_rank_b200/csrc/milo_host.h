@@ -1,6 +1,7 @@
 // milo_host.h -- host-side helpers of libmilo: error reporting and checks.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +19,12 @@ inline milo_status fail(milo_status s, const std::string& msg) {
     set_error(msg);
     return s;
 }
+
+// Tensor map of a 2-D row-major tensor [rows, cols] with row pitch `pitch`
+// bytes; box {bcols, brows} (api.cu).
+milo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+                     uint64_t pitch, uint32_t bcols, uint32_t brows, const char* what,
+                     CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 inline bool aligned(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) % a) == 0;
