@@ -171,8 +171,11 @@ def _stream(stream=None):
     return C.c_void_p(s.cuda_stream)
 
 
+_DT = {torch.float16: MILO_F16, torch.bfloat16: MILO_BF16, torch.float32: MILO_F32}
+
+
 def _dt(t: torch.Tensor) -> int:
-    return {torch.float16: MILO_F16, torch.bfloat16: MILO_BF16, torch.float32: MILO_F32}[t.dtype]
+    return _DT[t.dtype]
 
 
 def _cuda(t: torch.Tensor, name: str):
@@ -499,16 +502,16 @@ def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, log
     dev = ids.device
     T, k = ids.shape
     _arg(ids, "route['ids']", (torch.int32,))
-    _arg(w, "route['w']", (torch.float32,), shape=(T, k), device=dev)
-    _arg(dw, "dw", (torch.float32,), shape=(T, k), device=dev)
+    _need(w, "route['w']", (torch.float32,), (T, k), dev)
+    _need(dw, "dw", (torch.float32,), (T, k), dev)
     if logits is not None:
-        _arg(logits, "logits", (torch.float16,), shape=(T, E), device=dev)
+        _need(logits, "logits", (torch.float16,), (T, E), dev)
     elif not renorm:
         raise ValueError("milo_route_backward: logits are required without renorm")
     dlogits = _out(dlogits, "dlogits", (T, E), out_dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_route_backward", _ptr(logits), _ptr(ids), _ptr(w), _ptr(dw), T, E, k,
-            MILO_ROUTE_RENORM if renorm else 0, _ptr(dlogits), _dt(dlogits), _ptr(dev_status))
+    _launch(dev, "milo_route_backward", _p(logits), _p(ids), _p(w), _p(dw), T, E, k,
+            MILO_ROUTE_RENORM if renorm else 0, _p(dlogits), _dt(dlogits), _p(dev_status))
     return dlogits
 
 
@@ -516,15 +519,32 @@ def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, log
 # token rows in expert order
 # ---------------------------------------------------------------------------
 
+# The current stream's handle without building a Stream object (it costs
+# microseconds, as much as a small kernel).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
 def _launch(dev, name: str, *args):
     """Call a stream-ordered entry point on the current stream of `dev`."""
-    if dev.index == torch.cuda.current_device():
-        status = getattr(lib(), name)(*args, _stream())
-    else:
+    fn = getattr(_lib or lib(), name)
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, _stream())
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        status = fn(*args, _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream().cuda_stream)
     if status != MILO_OK:
         _check(status, name)
+
+
+def _need(t, name: str, dtypes, shape: tuple, device):
+    """_arg with its checks in one expression for a tensor that passes them."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device and
+            t.is_cuda and t.is_contiguous()):
+        _arg(t, name, dtypes, shape=shape, device=device)
 
 
 def _out(t, name: str, shape: tuple, dtype, device):
@@ -533,7 +553,7 @@ def _out(t, name: str, shape: tuple, dtype, device):
         if dtype not in _OUT:
             raise ValueError(f"{name} must be {' or '.join(_dname(d) for d in _OUT)}, not {_dname(dtype)}")
         return torch.empty(shape, dtype=dtype, device=device)
-    _arg(t, name, _OUT, shape=shape, device=device)
+    _need(t, name, _OUT, shape, device)
     return t
 
 
@@ -554,13 +574,13 @@ def _rows(t, name: str, rows: int, H: int | None, dtype, dev) -> int:
         raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
     if t.dim() != 2 or t.shape[0] != rows or (H is not None and t.shape[1] != H):
         raise ValueError(f"{name} must be [{rows}, {'H' if H is None else H}], not {tuple(t.shape)}")
-    _arg(t, name, _OUT if dtype is None else (dtype,), device=dev)
+    _need(t, name, _OUT if dtype is None else (dtype,), t.shape, dev)
     return t.shape[1]
 
 
 def _weights(w, T: int, k: int, dev):
     if w is not None:
-        _arg(w, "w", (torch.float32,), shape=(T, k), device=dev)
+        _need(w, "w", (torch.float32,), (T, k), dev)
 
 
 def milo_dispatch(x: torch.Tensor, route: dict, w: torch.Tensor | None = None, out_dtype=None,
@@ -574,7 +594,7 @@ def milo_dispatch(x: torch.Tensor, route: dict, w: torch.Tensor | None = None, o
     _weights(w, T, k, dev)
     xs = _out(xs, "xs", (T * k, H), out_dtype or x.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dispatch", _ptr(x), _dt(x), T, k, H, _ptr(inv), _ptr(w), _ptr(xs), _dt(xs), _ptr(dev_status))
+    _launch(dev, "milo_dispatch", _p(x), _dt(x), T, k, H, _p(inv), _p(w), _p(xs), _dt(xs), _p(dev_status))
     return xs
 
 
@@ -594,8 +614,8 @@ def milo_combine(ys: torch.Tensor, route: dict, w: torch.Tensor | None = None, r
     if residual is not None:
         _rows(residual, "residual", T, H, y.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_combine", _ptr(ys), _dt(ys), T, k, H, _ptr(inv), _ptr(w), _ptr(residual), _ptr(y), _dt(y),
-            _ptr(dev_status))
+    _launch(dev, "milo_combine", _p(ys), _dt(ys), T, k, H, _p(inv), _p(w), _p(residual), _p(y), _dt(y),
+            _p(dev_status))
     return y
 
 
@@ -615,8 +635,8 @@ def milo_dispatch_backward(dxs: torch.Tensor, route: dict, x: torch.Tensor | Non
         raise ValueError("milo_dispatch_backward: dw needs the call's w and x")
     dx = _out(dx, "dx", (T, H), out_dtype or dxs.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dispatch_backward", _ptr(dxs), _dt(dxs), T, k, H, _ptr(inv), _ptr(w),
-            None if dw is None else _ptr(x), _ptr(dx), _dt(dx), _ptr(dw), _ptr(dev_status))
+    _launch(dev, "milo_dispatch_backward", _p(dxs), _dt(dxs), T, k, H, _p(inv), _p(w),
+            None if dw is None else _p(x), _p(dx), _dt(dx), _p(dw), _p(dev_status))
     return dx, dw
 
 
@@ -638,15 +658,15 @@ def milo_combine_backward(dy: torch.Tensor, route: dict, ys: torch.Tensor | None
         raise ValueError("milo_combine_backward: dw needs the call's w and ys")
     dys = _out(dys, "dys", (T * k, H), out_dtype or dy.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_combine_backward", _ptr(dy), _dt(dy), T, k, H, _ptr(inv), _ptr(w),
-            None if dw is None else _ptr(ys), _ptr(dys), _dt(dys), _ptr(dw), _ptr(dev_status))
+    _launch(dev, "milo_combine_backward", _p(dy), _dt(dy), T, k, H, _p(inv), _p(w),
+            None if dw is None else _p(ys), _p(dys), _dt(dys), _p(dw), _p(dev_status))
     return dys, dw
 
 
 def _grad_w(dw, T: int, k: int, dev):
     if dw is None:
         return torch.empty((T, k), dtype=torch.float32, device=dev)
-    _arg(dw, "dw", (torch.float32,), shape=(T, k), device=dev)
+    _need(dw, "dw", (torch.float32,), (T, k), dev)
     return dw
 
 
@@ -682,17 +702,17 @@ def milo_dense_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | Non
     milo_dense_linear_backward."""
     M, N, K, dev, a = _dense_args(x, W, act)
     if bias is not None:
-        _arg(bias, "bias", (x.dtype,), shape=(N,), device=dev)
+        _need(bias, "bias", (x.dtype,), (N,), dev)
     if residual is not None and y is None and out_dtype is None:
         out_dtype = residual.dtype
     y = _out(y, "y", (M, N), out_dtype or x.dtype, dev)
     if residual is not None:
-        _arg(residual, "residual", (y.dtype,), shape=(M, N), device=dev)
+        _need(residual, "residual", (y.dtype,), (M, N), dev)
     if z is not None:
-        _arg(z, "z", (x.dtype,), shape=(M, N), device=dev)
+        _need(z, "z", (x.dtype,), (M, N), dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dense_linear", _ptr(x), _ptr(W), _dt(x), M, N, K, _ptr(bias), _ptr(residual), a, _ptr(y),
-            _dt(y), _ptr(z), _ptr(dev_status))
+    _launch(dev, "milo_dense_linear", _p(x), _p(W), _dt(x), M, N, K, _p(bias), _p(residual), a, _p(y),
+            _dt(y), _p(z), _p(dev_status))
     return y
 
 
@@ -712,9 +732,9 @@ def milo_dense_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tenso
     dy.  `out` may hold buffers for the gradients, `ws` a workspace of
     milo_dense_linear_backward_workspace_bytes."""
     M, N, K, dev, a = _dense_args(x, W, act)
-    _arg(dy, "dy", _OUT, shape=(M, N), device=dev)
+    _need(dy, "dy", _OUT, (M, N), dev)
     if z is not None:
-        _arg(z, "z", (x.dtype,), shape=(M, N), device=dev)
+        _need(z, "z", (x.dtype,), (M, N), dev)
     elif a != MILO_ACT_NONE:
         raise ValueError("milo_dense_linear_backward: z is required with an activation")
     shapes = {"dx": (M, K), "dW": (N, K), "db": (N,)}
@@ -732,9 +752,9 @@ def milo_dense_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tenso
         ws = torch.empty(milo_dense_linear_backward_workspace_bytes(M, N, K) + 256, dtype=torch.uint8, device=dev)
     wp, wn = _ws_arg(ws, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dense_linear_backward", _ptr(dy), _dt(dy), _ptr(x), _ptr(W), _dt(x), M, N, K, a, _ptr(z),
-            _ptr(grads.get("dx")), _ptr(grads.get("dW")), _ptr(grads.get("db")), C.c_void_p(wp), wn,
-            _ptr(dev_status))
+    _launch(dev, "milo_dense_linear_backward", _p(dy), _dt(dy), _p(x), _p(W), _dt(x), M, N, K, a, _p(z),
+            _p(grads.get("dx")), _p(grads.get("dW")), _p(grads.get("db")), wp, wn,
+            _p(dev_status))
     return grads
 
 

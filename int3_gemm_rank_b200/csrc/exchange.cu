@@ -1,19 +1,13 @@
-// exchange.cu -- token rows into expert order and back (milo_dispatch,
-// milo_combine, and their gradients' host side).
+// exchange.cu -- token rows into expert order (milo_dispatch), and the host side
+// of the way back and of the gradients (exchange_rows.cuh).
 //
 // "MiLo: Efficient Quantized MoE Inference with Mixture of Low-Rank
 // Compensators", "Background": an MoE layer sends each token to a subset of
 // its experts and mixes their outputs with the router's weights.  With f =
 // t*k + j the flat slot of token t's j-th pick and p = inv_perm[f] its row in
-// expert order:
-//     dispatch:  xs[p] = w[f] x[t]               (w optional)
-//     combine:   y[t]  = r[t] + sum_j w[f] ys[p]  (w, r optional)
-// Both walk the tokens, not the expert rows: dispatch then reads each token
-// row once for its k copies, and combine writes each output row once, its
-// sum in slot order in fp32.
-//
-// Bound by memory: dispatch moves T H + T k H elements, combine T k H + T H
-// (and T H of residual).
+// expert order: xs[p] = w[f] x[t] (w optional).  The kernel walks the tokens,
+// not the expert rows, so it reads each token row once for its k copies.
+// Bound by memory: T H elements read, T k H written.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,104 +20,63 @@ namespace milo {
 
 constexpr int kXThreads = 256;
 
-// One thread per (token, vector of V columns).
-template <typename TI, typename TO, int V>
+// Rows of whole 16-byte pieces: a thread takes U groups of eight columns, all
+// loaded before the first store.  (Other rows: exchange_rows.cuh.)
+template <typename TI, typename TO, int U>
 __global__ void __launch_bounds__(kXThreads) dispatch_kernel(const ExchangeParams p) {
     grid_dep_launch();
     grid_dep_wait();
-    const long long i = static_cast<long long>(blockIdx.x) * kXThreads + threadIdx.x;
-    if (i >= static_cast<long long>(p.T) * p.nv) return;
-    const int t = p.wide ? static_cast<int>(i / p.nv) : static_cast<int>(fast_div(static_cast<uint32_t>(i), p.div_m, p.div_s));
-    const uint32_t c = static_cast<uint32_t>(i - static_cast<long long>(t) * p.nv);
+    const long long i0 = static_cast<long long>(blockIdx.x) * (kXThreads * U) + threadIdx.x;
     const int rows = p.T * p.k;
     int32_t st = 0;
-    const RowVec<TI, V> x = load_vec<TI, V>(p.src, t, p.H, c);
-    for (int j = 0; j < p.k; ++j) {
-        const int f = t * p.k + j;
-        const int r = slot_row(p.inv_perm[f], rows, st);
-        if (r < 0) continue;
-        RowVec<TO, V> o;
-        const float w = p.w ? p.w[f] : 1.0f;
+    int t[U], c[U];
+    float x[U][8];
 #pragma unroll
-        for (int q = 0; q < V; ++q) o.v[q] = from_f32<TO>(w * to_f32(x.v[q]), st);
-        store_vec<TO, V>(p.out, r, p.H, c, o);
-    }
-    flag(p.dev_status, st);
-}
-
-// One thread per (token, vector of V columns): eight slots' rows in flight,
-// added in slot order.
-template <typename TI, typename TO, int V>
-__global__ void __launch_bounds__(kXThreads) combine_rows_kernel(const ExchangeParams p) {
-    grid_dep_launch();
-    grid_dep_wait();
-    const long long i = static_cast<long long>(blockIdx.x) * kXThreads + threadIdx.x;
-    if (i >= static_cast<long long>(p.T) * p.nv) return;
-    const int t = p.wide ? static_cast<int>(i / p.nv) : static_cast<int>(fast_div(static_cast<uint32_t>(i), p.div_m, p.div_s));
-    const uint32_t c = static_cast<uint32_t>(i - static_cast<long long>(t) * p.nv);
-    const int rows = p.T * p.k;
-    int32_t st = 0;
-    float acc[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-        int r[8];
-        float w[8];
-        RowVec<TI, V> v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r[j] = -1;
-            if (j0 + j < p.k) {
-                const int f = t * p.k + j0 + j;
-                r[j] = slot_row(p.inv_perm[f], rows, st);
-                w[j] = p.w ? p.w[f] : 1.0f;
-            }
+    for (int u = 0; u < U; ++u) {
+        const long long i = i0 + u * kXThreads;
+        t[u] = -1;
+        if (i < static_cast<long long>(p.T) * p.nv) {
+            t[u] = p.wide ? static_cast<int>(i / p.nv)
+                          : static_cast<int>(fast_div(static_cast<uint32_t>(i), p.div_m, p.div_s));
+            c[u] = static_cast<int>(i - static_cast<long long>(t[u]) * p.nv) * 8;
+            load8<TI>(static_cast<const TI*>(p.src) + static_cast<long long>(t[u]) * p.H + c[u], x[u]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (r[j] >= 0) v[j] = load_vec<TI, V>(p.src, r[j], p.H, c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (r[j] >= 0) {
-#pragma unroll
-                for (int q = 0; q < V; ++q) acc[q] = fmaf(w[j], to_f32(v[j].v[q]), acc[q]);
-            }
     }
-    if (p.other) {
-        const RowVec<TO, V> res = load_vec<TO, V>(p.other, t, p.H, c);
 #pragma unroll
-        for (int q = 0; q < V; ++q) acc[q] += to_f32(res.v[q]);
+    for (int u = 0; u < U; ++u) {
+        if (t[u] < 0) continue;
+        for (int j = 0; j < p.k; ++j) {
+            const int f = t[u] * p.k + j;
+            const int r = slot_row(p.inv_perm[f], rows, st);
+            if (r < 0) continue;
+            const float w = p.w ? p.w[f] : 1.0f;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = w * x[u][q];
+            store8<TO>(static_cast<TO*>(p.out) + static_cast<long long>(r) * p.H + c[u], o, st);
+        }
     }
-    RowVec<TO, V> o;
-#pragma unroll
-    for (int q = 0; q < V; ++q) o.v[q] = from_f32<TO>(acc[q], st);
-    store_vec<TO, V>(p.out, t, p.H, c, o);
     flag(p.dev_status, st);
-}
-
-template <typename TI, typename TO, int V>
-static cudaError_t run_exchange(const ExchangeParams& p, bool combine, cudaStream_t s) {
-    const long long blocks = (static_cast<long long>(p.T) * p.nv + kXThreads - 1) / kXThreads;
-    return launch_pdl(combine ? combine_rows_kernel<TI, TO, V> : dispatch_kernel<TI, TO, V>,
-                      dim3(static_cast<unsigned>(blocks)), dim3(kXThreads), 0, s, p);
 }
 
 template <typename TI, typename TO>
-static cudaError_t run_exchange_v(const ExchangeParams& p, int vec, bool combine, cudaStream_t s) {
-    return vec == 8 ? run_exchange<TI, TO, 8>(p, combine, s) : run_exchange<TI, TO, 1>(p, combine, s);
+static cudaError_t run_dispatch(const ExchangeParams& p, cudaStream_t s) {
+    constexpr int U = 2;
+    const long long blocks = (static_cast<long long>(p.T) * p.nv + kXThreads * U - 1) / (kXThreads * U);
+    return launch_pdl(dispatch_kernel<TI, TO, U>, dim3(static_cast<unsigned>(blocks)), dim3(kXThreads), 0, s, p);
 }
 
-template <typename TI>
-static cudaError_t run_exchange_o(const ExchangeParams& p, const ExchangeTypes& t, bool combine, cudaStream_t s) {
-    if (t.out == MILO_F32) return run_exchange_v<TI, float>(p, t.vec, combine, s);
-    if (t.out == MILO_F16) return run_exchange_v<TI, __half>(p, t.vec, combine, s);
-    return run_exchange_v<TI, __nv_bfloat16>(p, t.vec, combine, s);
-}
-
-cudaError_t launch_exchange(const ExchangeParams& p, const ExchangeTypes& t, bool combine, cudaStream_t s) {
-    if (t.in == MILO_F32) return run_exchange_o<float>(p, t, combine, s);
-    if (t.in == MILO_F16) return run_exchange_o<__half>(p, t, combine, s);
-    return run_exchange_o<__nv_bfloat16>(p, t, combine, s);
+cudaError_t launch_dispatch(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s) {
+    if (!t.aligned) return launch_dispatch_rows(p, t, s);
+    auto by_out = [&](auto in) {
+        using TI = decltype(in);
+        if (t.out == MILO_F32) return run_dispatch<TI, float>(p, s);
+        if (t.out == MILO_F16) return run_dispatch<TI, __half>(p, s);
+        return run_dispatch<TI, __nv_bfloat16>(p, s);
+    };
+    if (t.in == MILO_F32) return by_out(float{});
+    if (t.in == MILO_F16) return by_out(__half{});
+    return by_out(__nv_bfloat16{});
 }
 
 // ---------------------------------------------------------------------------
@@ -142,23 +95,21 @@ static milo_status check_exchange(const char* what, milo_dtype in, milo_dtype ou
     if (H > kMaxProjK) return fail(MILO_ERR_UNSUPPORTED_SHAPE, f + ": H above 2^24");
     if (static_cast<long long>(T) * k > MILO_MAX_ROWS)
         return fail(MILO_ERR_UNSUPPORTED_SHAPE, f + ": T*k above MILO_MAX_ROWS");
-    // one block per 256 elements of the token rows at the least
+    // the kernels' blocks, 256 vectors of eight columns each at the least, stay a 31-bit count
     if (static_cast<long long>(T) * H > (1LL << 38))
         return fail(MILO_ERR_UNSUPPORTED_SHAPE, f + ": T*H above 2^38");
     return MILO_OK;
 }
 
-// The 16-byte path needs rows of whole 16-byte pieces at 16-byte addresses;
-// every other width or address goes element by element.
-static int exchange_vec(int H, std::initializer_list<const void*> ptrs) {
-    if (H % 8) return 1;
+static bool exchange_aligned(int H, std::initializer_list<const void*> ptrs) {
+    if (H % 8) return false;
     for (const void* q : ptrs)
-        if (q && !aligned(q, 16)) return 1;
-    return 8;
+        if (q && !aligned(q, 16)) return false;
+    return true;
 }
 
-static void exchange_index(ExchangeParams& p, int vec) {
-    p.nv = static_cast<uint32_t>(p.H / vec);
+static void exchange_index(ExchangeParams& p) {
+    p.nv = static_cast<uint32_t>((p.H + 7) / 8);
     uint32_t s = 0;
     while ((1ULL << s) < p.nv) ++s;
     p.div_s = s;
@@ -186,10 +137,10 @@ extern "C" milo_status milo_dispatch(const void* x, milo_dtype x_dt, int32_t T, 
     if (T == 0) return MILO_OK;
     if (!x || !xs || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_dispatch: NULL pointer");
     if ((s = check_rows("milo_dispatch", {{x, x_dt}, {xs, xs_dt}})) != MILO_OK) return s;
-    const ExchangeTypes ty{x_dt, xs_dt, exchange_vec(H, {x, xs})};
+    const ExchangeTypes ty{x_dt, xs_dt, exchange_aligned(H, {x, xs})};
     ExchangeParams p = {x, nullptr, inv_perm, w, xs, nullptr, dev_status, T, k, H, 0, 0, 0, 0};
-    exchange_index(p, ty.vec);
-    return check_cuda(launch_exchange(p, ty, false, static_cast<cudaStream_t>(stream)), "milo_dispatch");
+    exchange_index(p);
+    return check_cuda(launch_dispatch(p, ty, static_cast<cudaStream_t>(stream)), "milo_dispatch");
 }
 
 extern "C" milo_status milo_combine(const void* ys, milo_dtype ys_dt, int32_t T, int32_t k, int32_t H,
@@ -201,10 +152,10 @@ extern "C" milo_status milo_combine(const void* ys, milo_dtype ys_dt, int32_t T,
     if (T == 0) return MILO_OK;
     if (!ys || !y || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_combine: NULL pointer");
     if ((s = check_rows("milo_combine", {{ys, ys_dt}, {y, y_dt}, {residual, y_dt}})) != MILO_OK) return s;
-    const ExchangeTypes ty{ys_dt, y_dt, exchange_vec(H, {ys, y, residual})};
+    const ExchangeTypes ty{ys_dt, y_dt, exchange_aligned(H, {ys, y, residual})};
     ExchangeParams p = {ys, residual, inv_perm, w, y, nullptr, dev_status, T, k, H, 0, 0, 0, 0};
-    exchange_index(p, ty.vec);
-    return check_cuda(launch_exchange(p, ty, true, static_cast<cudaStream_t>(stream)), "milo_combine");
+    exchange_index(p);
+    return check_cuda(launch_combine_rows(p, ty, static_cast<cudaStream_t>(stream)), "milo_combine");
 }
 
 extern "C" milo_status milo_dispatch_backward(const void* dxs, milo_dtype dxs_dt, int32_t T, int32_t k, int32_t H,
@@ -219,14 +170,14 @@ extern "C" milo_status milo_dispatch_backward(const void* dxs, milo_dtype dxs_dt
     if (!dxs || !dx || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_dispatch_backward: NULL pointer");
     if ((s = check_rows("milo_dispatch_backward", {{dxs, dxs_dt}, {dx, dx_dt}, {dw ? x : nullptr, dxs_dt}})) != MILO_OK)
         return s;
-    const ExchangeTypes ty{dxs_dt, dx_dt, exchange_vec(H, {dxs, dx, dw ? x : nullptr})};
+    const ExchangeTypes ty{dxs_dt, dx_dt, exchange_aligned(H, {dxs, dx, dw ? x : nullptr})};
     ExchangeParams p = {dxs, nullptr, inv_perm, w, dx, dw, dev_status, T, k, H, 0, 0, 0, 0};
-    exchange_index(p, ty.vec);
+    exchange_index(p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // without a weight gradient this is the combine of the gradients' rows
-    if (!dw) return check_cuda(launch_exchange(p, ty, true, st), "milo_dispatch_backward");
+    if (!dw) return check_cuda(launch_combine_rows(p, ty, st), "milo_dispatch_backward");
     p.other = x;
-    return check_cuda(launch_exchange_grad(p, ty, false, st), "milo_dispatch_backward");
+    return check_cuda(launch_dispatch_grad(p, ty, st), "milo_dispatch_backward");
 }
 
 extern "C" milo_status milo_combine_backward(const void* dy, milo_dtype dy_dt, int32_t T, int32_t k, int32_t H,
@@ -241,12 +192,12 @@ extern "C" milo_status milo_combine_backward(const void* dy, milo_dtype dy_dt, i
     if (!dy || !dys || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_combine_backward: NULL pointer");
     if ((s = check_rows("milo_combine_backward", {{dy, dy_dt}, {dys, dys_dt}, {dw ? ys : nullptr, dy_dt}})) != MILO_OK)
         return s;
-    const ExchangeTypes ty{dy_dt, dys_dt, exchange_vec(H, {dy, dys, dw ? ys : nullptr})};
+    const ExchangeTypes ty{dy_dt, dys_dt, exchange_aligned(H, {dy, dys, dw ? ys : nullptr})};
     ExchangeParams p = {dy, nullptr, inv_perm, w, dys, dw, dev_status, T, k, H, 0, 0, 0, 0};
-    exchange_index(p, ty.vec);
+    exchange_index(p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // without a weight gradient this is the dispatch of the output's gradient
-    if (!dw) return check_cuda(launch_exchange(p, ty, false, st), "milo_combine_backward");
+    if (!dw) return check_cuda(launch_dispatch(p, ty, st), "milo_combine_backward");
     p.other = ys;
-    return check_cuda(launch_exchange_grad(p, ty, true, st), "milo_combine_backward");
+    return check_cuda(launch_combine_grad(p, ty, st), "milo_combine_backward");
 }

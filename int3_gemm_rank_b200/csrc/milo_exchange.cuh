@@ -1,9 +1,11 @@
 // milo_exchange.cuh -- pieces shared by the kernels that move token rows into
-// expert order and back (exchange.cu) and their gradients (exchange_grad.cu).
+// expert order and back and their gradients (exchange.cu, exchange_rows.cuh).
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "milo_device.cuh"
 
@@ -18,7 +20,7 @@ struct ExchangeParams {
     float* dw;                  // gradients: [T*k] or NULL
     int32_t* dev_status;
     int T, k, H;
-    uint32_t nv;                // H / V: vectors of a row
+    uint32_t nv;                // ceil(H / 8): vectors of a row
     uint32_t div_m, div_s;      // i / nv for i < 2^31 (see fast_div)
     int wide;                   // T * nv does not fit 31 bits: 64-bit indices
 };
@@ -52,36 +54,69 @@ __device__ __forceinline__ __half from_f32<__half>(float v, int32_t& st) {
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v, int32_t&) { return __float2bfloat16_rn(v); }
 
-// V consecutive elements, moved in 16-byte pieces (V = 8; the address is
-// 16-byte aligned) or one element at a time (V = 1).
-template <typename T, int V>
-struct alignas(V == 1 ? sizeof(T) : 16) RowVec {
-    T v[V];
-};
-
-template <typename T, int V>
-__device__ __forceinline__ RowVec<T, V> load_vec(const void* base, size_t row, size_t H, uint32_t c) {
-    RowVec<T, V> r;
-    const T* p = static_cast<const T*>(base) + row * H + static_cast<size_t>(c) * V;
-    if constexpr (V == 1) {
-        r.v[0] = *p;
-    } else {
-#pragma unroll
-        for (int q = 0; q < static_cast<int>(V * sizeof(T) / 16); ++q)
-            reinterpret_cast<uint4*>(r.v)[q] = reinterpret_cast<const uint4*>(p)[q];
-    }
-    return r;
+// Two fp32 values rounded to 16 bits each, as one word.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(void* base, size_t row, size_t H, uint32_t c, const RowVec<T, V>& r) {
-    T* p = static_cast<T*>(base) + row * H + static_cast<size_t>(c) * V;
-    if constexpr (V == 1) {
-        *p = r.v[0];
+// Eight values to a 16-byte aligned address.  FP16_RANGE: a half whose exponent
+// field is all ones (adding one there carries into the sign's place) is looked
+// at again, since an infinity may have been one before.
+template <typename T>
+__device__ __forceinline__ void store8(void* dst, const float (&v)[8], int32_t& st) {
+    if constexpr (sizeof(T) == 4) {
+        float4* d = static_cast<float4*>(dst);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < static_cast<int>(V * sizeof(T) / 16); ++q)
-            reinterpret_cast<uint4*>(p)[q] = reinterpret_cast<const uint4*>(r.v)[q];
+        for (int q = 0; q < 4; ++q) w[q] = pack2<T>(v[2 * q], v[2 * q + 1]);
+        if constexpr (std::is_same<T, __half>::value) {
+            uint32_t e = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e |= (w[q] & 0x7C007C00u) + 0x04000400u;
+            if (e & 0x80008000u) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (fabsf(v[q]) >= 65520.0f && !isinf(v[q])) st |= MILO_DEV_FP16_RANGE;
+            }
+        }
+        *static_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Eight values from a 16-byte aligned address.
+template <typename T>
+__device__ __forceinline__ void load8(const void* src, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4* p = static_cast<const float4*>(src);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = *static_cast<const uint4*>(src);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+                v[2 * q] = f.x;
+                v[2 * q + 1] = f.y;
+            } else {
+                v[2 * q] = __uint_as_float(w[q] << 16);
+                v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+            }
+        }
     }
 }
 
@@ -95,10 +130,13 @@ __device__ __forceinline__ int slot_row(int r, int rows, int32_t& st) {
 
 struct ExchangeTypes {
     milo_dtype in, out;
-    int vec;                    // 8 or 1
+    bool aligned;               // rows of whole 16-byte pieces at 16-byte addresses
 };
 
-cudaError_t launch_exchange(const ExchangeParams& p, const ExchangeTypes& t, bool combine, cudaStream_t s);
-cudaError_t launch_exchange_grad(const ExchangeParams& p, const ExchangeTypes& t, bool combine, cudaStream_t s);
+cudaError_t launch_dispatch(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s);
+cudaError_t launch_dispatch_rows(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s);
+cudaError_t launch_combine_rows(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s);
+cudaError_t launch_combine_grad(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s);
+cudaError_t launch_dispatch_grad(const ExchangeParams& p, const ExchangeTypes& t, cudaStream_t s);
 
 }  // namespace milo

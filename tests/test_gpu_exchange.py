@@ -114,6 +114,49 @@ def test_unaligned_rows_and_residual_in_place(milo):
     check(y, *want, "in place")
 
 
+@pytest.mark.parametrize("dt,out", [("bf16", "f32"), ("f32", "f32"), ("f32", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("H", [1, 3, 5, 8, 13, 263, 515])
+@pytest.mark.parametrize("so,oo", [(0, 0), (1, 0), (0, 3), (5, 2)])
+def test_rows_that_start_anywhere(milo, dt, out, H, so, oo):
+    """Inputs and outputs at every kind of offset inside larger buffers, widths
+    that shift every row: results right, and nothing beside the outputs is
+    written."""
+    rng = np.random.default_rng(H)
+    T, k, E = 9, 3, 6
+    r = make_route(milo, rng, T, k, E, "some")
+    inv = r["inv_perm"].cpu().numpy().reshape(T, k).astype(int)
+    w = n64(r["w"])
+
+    def inside(rows, d, off):
+        buf = rand(rng, (rows * H + off + 16,), d)
+        return buf, buf[off:off + rows * H].view(rows, H)
+
+    _, x = inside(T, dt, so)
+    _, rows = inside(T * k, dt, so)
+    for name in ("dispatch", "combine", "dispatch_backward", "combine_backward"):
+        expert = name in ("dispatch", "combine_backward")
+        n = T * k if expert else T
+        buf, o = inside(n, out, oo)
+        before, was = buf.clone(), n64(o)
+        _, res = inside(T, out, so)
+        if name == "dispatch":
+            milo.milo_dispatch(x, r, r["w"], xs=o)
+            want = R.dispatch(n64(x), inv, w, out, was)
+        elif name == "combine":
+            milo.milo_combine(rows, r, r["w"], res, y=o)
+            want = R.combine(n64(rows), inv, w, n64(res), out)
+        elif name == "dispatch_backward":
+            _, dw = milo.milo_dispatch_backward(rows, r, x, r["w"], dx=o)
+            want = R.combine(n64(rows), inv, w, None, out)
+            check(dw, *R.slot_dots(n64(x), n64(rows), inv), name)
+        else:
+            _, dw = milo.milo_combine_backward(x, r, rows, r["w"], dys=o)
+            want = R.dispatch(n64(x), inv, w, out, was)
+            check(dw, *R.slot_dots(n64(x), n64(rows), inv), name)
+        check(o, *want, name)
+        assert torch.equal(buf[:oo], before[:oo]) and torch.equal(buf[oo + n * H:], before[oo + n * H:]), name
+
+
 def test_bad_rows_are_flagged_and_skipped(milo):
     rng = np.random.default_rng(8)
     T, k, H = 4, 2, 32
