@@ -19,8 +19,8 @@
 // products run in fp32 in a fixed order.
 //
 // A row that starts off a 16-byte boundary comes in the aligned pieces that
-// cover it; its columns are then read and written one element per lane
-// (lane, lane + 32, ...), which no misalignment slows down.
+// cover it; its columns are then read one element per lane (lane, lane + 32,
+// ...), which no misalignment slows down, and written the same way.
 #pragma once
 
 #include <algorithm>
@@ -34,7 +34,8 @@ namespace milo {
 
 enum { kXDispatch, kXCombine, kXCombineGrad, kXDispatchGrad };
 
-constexpr int kXrWarps = 8;
+constexpr int kXrWarps = 12;
+constexpr int kXrTeams[] = {1, 2, 4};        // warps that may share a token's pieces (gradients)
 constexpr int kXrThreads = 32 * kXrWarps;
 constexpr int kXrStages = 2;
 constexpr int kXrSlack = 32;                 // bytes a row that starts off a 16-byte boundary may add
@@ -44,6 +45,7 @@ struct XRowsParams {
     ExchangeParams x;
     int cols, nch;              // columns of a piece (a multiple of 64), pieces of a row
     int pitch, nrows;           // bytes between a stage's rows; rows of a stage
+    int team;                   // gradients: warps per token
 };
 
 struct alignas(16) XMeta {      // a live slot of a stage
@@ -115,11 +117,20 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
     __shared__ uint64_t full[kXrWarps][kXrStages];
     __shared__ XMeta meta[kXrWarps][kXrStages][KM + 1];                      // live slots, then the token's row
     __shared__ int live[kXrWarps][kXrStages];
+    // gradients with several warps per token: their partial dot products, two
+    // tokens deep (filled: all but the leader have written; taken: read)
+    __shared__ float part[kDot ? kXrWarps : 1][2][KM];
+    __shared__ uint64_t filled[kXrWarps][2], taken[kXrWarps][2];
     const ExchangeParams& p = P.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_launch();
     if (lane < kXrStages) mbar_init(&full[warp][lane], 1);
+    if (kDot && lane < 2) {
+        mbar_init(&filled[warp][lane], max(1, P.team - 1));
+        mbar_init(&taken[warp][lane], 1);
+    }
     fence_barrier_init();
+    if (kDot && P.team > 1) __syncthreads();      // the barriers of the team's first warp
     __syncwarp();
     grid_dep_wait();
 
@@ -130,18 +141,21 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
     const bool has_tok = MODE != kXCombine || p.other;
     const int tok_at = kLoadRows ? p.k : 0;                                  // the token's row of a stage
     uint8_t* ring = smem + static_cast<size_t>(warp) * kXrStages * P.nrows * P.pitch;
-    // the pieces of all tokens are spread over the warps, but a token's pieces
-    // stay on one warp where its registers hold the dot products
-    const int gw = static_cast<int>(blockIdx.x) * kXrWarps + warp, nw = static_cast<int>(gridDim.x) * kXrWarps;
+    // The pieces of all tokens are spread over the warps, over the blocks first.
+    // A gradient's token belongs to a team of warps of one block, whose
+    // registers hold its dot products: member g takes pieces g, g + team, ...
+    const int team = kDot ? P.team : 1, g = kDot ? warp % team : 0, lead = warp - g;
+    const int gw = warp / team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    const int nw = kXrWarps / team * static_cast<int>(gridDim.x);
     struct Cursor {
         int t, ch;
     };
-    const int dt = kDot ? 0 : nw / P.nch, dch = kDot ? 1 : nw - nw / P.nch * P.nch;
+    const int dt = kDot ? 0 : nw / P.nch, dch = kDot ? team : nw - nw / P.nch * P.nch;
     auto advance = [&](Cursor& c) {
         c.ch += dch;
         c.t += dt;
         if (c.ch >= P.nch) {
-            c.ch -= P.nch;
+            c.ch = kDot ? g : c.ch - P.nch;
             c.t += kDot ? nw : 1;
         }
     };
@@ -156,7 +170,7 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
             nwt = p.w ? p.w[c.t * p.k + lane] : 1.0f;
         }
     };
-    Cursor head{kDot ? gw : gw / P.nch, kDot ? 0 : gw - gw / P.nch * P.nch};
+    Cursor head{kDot ? gw : gw / P.nch, kDot ? g : gw - gw / P.nch * P.nch};
     Cursor tail = head;
     auto issue = [&](int s) {
         const int c0 = head.ch * P.cols, nc = min(P.cols, p.H - c0);
@@ -199,15 +213,21 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
     fetch(head);
     for (int s = 0; s < kXrStages; ++s)
         if (head.t < p.T) issue(s);
-    int s = 0;
+    int s = 0, nth = 0, under_way = kXrStages;
     uint32_t phase = 0;
+    bool drain = false;
     while (tail.t < p.T) {
         if (!warp_wait(&full[warp][s], phase)) {
             st |= MILO_DEV_TIMEOUT;
-            // the other stage's copies land before the block leaves
+            drain = true;
+        }
+        if (drain) {
+            // the copies under way land before the block leaves
+            if (head.t < p.T) head.t = p.T;
             advance(tail);
-            if (tail.t < p.T) warp_wait(&full[warp][s ^ 1], s ? phase ^ 1 : phase);
-            break;
+            if (tail.t >= p.T || --under_way <= 0) break;
+            if (++s == kXrStages) { s = 0; phase ^= 1; }
+            continue;
         }
         const int t = tail.t, c0 = tail.ch * P.cols, nc = min(P.cols, p.H - c0);
         const uint8_t* stage = ring + s * P.nrows * P.pitch;
@@ -262,8 +282,9 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
             }
         }
         if constexpr (kDot) {
-            if (tail.ch == P.nch - 1) {
-                // the token's last piece: its dot products, 0 for a dropped slot
+            if (tail.ch + team >= P.nch) {
+                // this warp's last piece of the token: the sums over its lanes, to
+                // lane j for live slot j
                 float mine = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KM; ++j) {
@@ -271,11 +292,36 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
                         float d = dot[j];
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-                        if (lane == mt[j].slot) mine = d;
+                        if (lane == j) mine = d;
                     }
                     dot[j] = 0.0f;
                 }
-                if (lane < p.k) p.dw[t * p.k + lane] = mine;
+                bool ok = true;
+                if (g > 0) {
+                    // a member: its sums to the leader, once the token two before has been read
+                    ok = warp_wait(&taken[lead][nth & 1], ((nth >> 1) & 1) ^ 1);
+                    if (ok) {
+                        if (lane < KM) part[warp][nth & 1][lane] = mine;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&filled[lead][nth & 1]);
+                    }
+                } else {
+                    if (team > 1) {
+                        ok = warp_wait(&filled[lead][nth & 1], (nth >> 1) & 1);
+                        for (int q = 1; q < team; ++q)
+                            if (lane < KM) mine += part[lead + q][nth & 1][lane];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&taken[lead][nth & 1]);
+                    }
+                    if (lane < p.k) p.dw[t * p.k + lane] = 0.0f;        // a dropped slot keeps this
+                    __syncwarp();
+                    if (lane < cnt) p.dw[t * p.k + mt[lane].slot] = mine;
+                }
+                if (!ok) {
+                    st |= MILO_DEV_TIMEOUT;
+                    drain = true;
+                }
+                ++nth;
             }
         }
         __syncwarp();
@@ -299,8 +345,9 @@ inline cudaError_t launch_rows(const XRowsParams& P, size_t smem, cudaStream_t s
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
     }
-    const long long items = static_cast<long long>(P.x.T) * (MODE == kXCombine || MODE == kXDispatch ? P.nch : 1);
-    const long long grid = std::min<long long>(sms, (items + kXrWarps - 1) / kXrWarps);
+    const bool dot = MODE == kXCombineGrad || MODE == kXDispatchGrad;
+    const long long items = static_cast<long long>(P.x.T) * (dot ? 1 : P.nch);
+    const long long grid = std::min<long long>(sms, items);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kXrThreads), smem, s, P);
 }
 
@@ -310,12 +357,34 @@ inline cudaError_t run_rows(const ExchangeParams& p, bool al, cudaStream_t s) {
     XRowsParams P;
     P.x = p;
     P.nrows = MODE == kXDispatch ? 1 : p.k + (MODE != kXCombine || p.other ? 1 : 0);
-    // pieces as long as the ring allows, a row cut evenly, whole groups of 64 columns
     const int slack = al ? 0 : kXrSlack;
     const int max_cols = ((kXrSmem / (kXrWarps * kXrStages * P.nrows) - slack) / es) / 64 * 64;
-    P.nch = (p.H + max_cols - 1) / max_cols;
-    P.cols = std::min(max_cols, ((p.H + P.nch - 1) / P.nch + 63) / 64 * 64);
-    P.nch = (p.H + P.cols - 1) / P.cols;
+    // Piece length (b blocks of 256 columns, as the ring allows) and team: the
+    // work is dealt out in whole items, so what counts is how evenly they fill
+    // the warps' rounds, against a fixed cost per item (0.15 us of a warp) and,
+    // with teams, per token; a block of 256 columns costs 0.14 us per row moved
+    // (12 warps sharing an SM's part of the bandwidth).
+    const bool dot = MODE == kXCombineGrad || MODE == kXDispatchGrad;
+    const double rows_moved = (MODE == kXDispatch ? 1 : p.k + 1) + (MODE == kXCombineGrad || MODE == kXDispatch ? p.k : 1);
+    const long long nw = 148LL * kXrWarps;
+    double best = -1.0;
+    for (int b = std::max(1, max_cols / 256); b >= 1; --b) {
+        const int cols = std::min(max_cols, 256 * b), nch = (p.H + cols - 1) / cols;
+        for (int team : kXrTeams) {
+            if (team > 1 && (!dot || team > nch)) break;
+            const long long warps = nw / team;
+            const long long items = dot ? (p.T + warps - 1) / warps * ((nch + team - 1) / team)
+                                        : (static_cast<long long>(p.T) * nch + nw - 1) / nw;
+            double cost = items * (0.15 + 0.14 * rows_moved * std::min(b, (p.H + 255) / 256));
+            if (team > 1) cost += 0.2 * ((p.T + warps - 1) / warps);
+            if (best < 0.0 || cost < best * 0.999) {
+                best = cost;
+                P.cols = cols;
+                P.nch = nch;
+                P.team = team;
+            }
+        }
+    }
     P.pitch = P.cols * es + slack;
     const size_t smem = static_cast<size_t>(kXrWarps) * kXrStages * P.nrows * P.pitch;
     if (MODE != kXDispatch && al) {

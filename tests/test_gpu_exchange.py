@@ -52,7 +52,7 @@ def check(got, want, bound, what):
 # H: one column, odd, even, 16-byte rows shorter and longer than a block's pass
 CASES = [(1, 1, 1, 1, "none"), (1, 2, 4096, 8, "none"), (3, 3, 7, 5, "some"), (16, 2, 64, 8, "none"),
          (37, 6, 2051, 64, "some"), (50, 16, 264, 16, "some"), (9, 9, 514, 200, "none"), (5, 2, 40, 4, "all"),
-         (130, 8, 1024, 256, "none"), (2, 4, 8200, 4, "some")]
+         (130, 8, 1024, 256, "none"), (2, 4, 8200, 4, "some"), (1900, 2, 1032, 8, "some"), (1000, 3, 771, 8, "some")]
 
 
 @pytest.mark.parametrize("T,k,H,E,drop", CASES)
