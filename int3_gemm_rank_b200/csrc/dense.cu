@@ -24,7 +24,8 @@ namespace milo {
 // dz = dy act'(z), and its column sums
 // ---------------------------------------------------------------------------
 constexpr int kDzRows = 64;         // rows of a block
-constexpr int kDzThreads = 256;
+constexpr int kDzCols = 256;        // columns of a block
+constexpr int kDzThreads = 256;     // 32 groups of eight columns by 8 row lanes
 
 struct DzParams {
     const void* dy;             // [M, N] in dy_dt
@@ -33,29 +34,86 @@ struct DzParams {
     float* part;                // [row blocks][N] column sums, or NULL
     int32_t* dev_status;
     int M, N, ldz, dy_dt, bf16, act;
+    int vec;                    // dy and z in whole 16-byte pieces
+    int col_blocks;
 };
 
-// One block: kDzRows rows of 256 columns, a thread per column, so the column
-// sum is the thread's own (fp32, row order).
+// Eight columns n.. of row m: 16-byte loads where rows allow them.
+__device__ __forceinline__ void dz_load8(const void* p, size_t row, int N, int n, int dt, int vec, float (&v)[8]) {
+    const size_t i = row * N + n;
+    if (vec && n < N) {
+        if (dt == MILO_F32) {
+            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+            const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = act_f32(static_cast<uint16_t>(q & 1 ? w[q / 2] >> 16 : w[q / 2] & 0xFFFFu), dt == MILO_BF16);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = n + q < N ? load_any(p, i + q, dt) : 0.0f;
+    }
+}
+
+// One block: kDzRows rows of 256 columns.  A thread takes eight columns of
+// every eighth row; the column sums of its rows are its own, and the eight row
+// lanes meet in shared memory in lane order.  Bound by memory: dy and z read,
+// dz written once.
 __global__ void __launch_bounds__(kDzThreads) dense_dz_kernel(const DzParams p) {
+    __shared__ float red[8][kDzCols];
     grid_dep_launch();
     grid_dep_wait();
-    const int n = blockIdx.y * kDzThreads + threadIdx.x;
-    const int m0 = blockIdx.x * kDzRows;
-    if (n >= (p.dz ? p.ldz : p.N)) return;
+    const int col = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
+    const int rb = static_cast<int>(blockIdx.x) / p.col_blocks, cb = static_cast<int>(blockIdx.x) % p.col_blocks;
+    const int n = cb * kDzCols + col;
+    const int m1 = min(p.M, (rb + 1) * kDzRows);
     int32_t st = 0;
-    float sum = 0.0f;
-    for (int m = m0; m < min(p.M, m0 + kDzRows); ++m) {
-        float v = 0.0f;
-        if (n < p.N) {
-            const size_t i = static_cast<size_t>(m) * p.N + n;
-            v = load_any(p.dy, i, p.dy_dt);
-            if (p.z) v *= dense_dact(p.act, load16(p.z, i, p.bf16));
-        }
-        sum += v;
-        if (p.dz) static_cast<uint16_t*>(p.dz)[static_cast<size_t>(m) * p.ldz + n] = round16(v, p.bf16, st);
+    float sum[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
+    if (n < p.ldz) {
+        with_act(p.act, [&](auto act) {
+            constexpr int A = decltype(act)::value;
+#pragma unroll 2
+            for (int m = rb * kDzRows + rl; m < m1; m += 8) {
+                float v[8];
+                dz_load8(p.dy, m, p.N, n, p.dy_dt, p.vec, v);
+                if constexpr (A != MILO_ACT_NONE) {
+                    float z[8];
+                    dz_load8(p.z, m, p.N, n, p.bf16 ? MILO_BF16 : MILO_F16, p.vec, z);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] *= act_slope<A>(z[q]);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sum[q] += v[q];
+                if (p.dz) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = static_cast<uint32_t>(round16(v[2 * q], p.bf16, st)) |
+                               (static_cast<uint32_t>(round16(v[2 * q + 1], p.bf16, st)) << 16);
+                    // the scratch rows are whole 16-byte pieces
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + static_cast<size_t>(m) * p.ldz + n) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        });
     }
-    if (p.part && n < p.N) p.part[static_cast<size_t>(blockIdx.x) * p.N + n] = sum;
+    if (p.part) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) red[rl][col + q] = sum[q];
+        __syncthreads();
+        const int nc = cb * kDzCols + threadIdx.x;
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += red[q][threadIdx.x];
+        if (nc < p.N) p.part[static_cast<size_t>(rb) * p.N + nc] = s;
+    }
     flag(p.dev_status, st);
 }
 
@@ -177,9 +235,9 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
     if (want_dz || db) {
         DzParams p = {dy, act == MILO_ACT_NONE ? nullptr : z, want_dz ? base + w.dz : nullptr,
                       db ? reinterpret_cast<float*>(base + w.part) : nullptr, dev_status, M, N, w.ldz,
-                      static_cast<int>(dy_dt), dt == MILO_BF16, act};
-        const dim3 grid(static_cast<unsigned>(w.blocks), static_cast<unsigned>((w.ldz + kDzThreads - 1) / kDzThreads));
-        if (grid.y > 65535) return fail(MILO_ERR_UNSUPPORTED_SHAPE, "milo_dense_linear_backward: N too large");
+                      static_cast<int>(dy_dt), dt == MILO_BF16, act,
+                      N % 8 == 0 && aligned(dy, 16) && (act == MILO_ACT_NONE || aligned(z, 16)), (w.ldz + kDzCols - 1) / kDzCols};
+        const dim3 grid(static_cast<unsigned>(w.blocks) * static_cast<unsigned>(p.col_blocks));
         if ((s = check_cuda(launch_pdl(dense_dz_kernel, grid, dim3(kDzThreads), 0, st, p), "dz")) != MILO_OK) return s;
     }
     if (db) {

@@ -176,10 +176,7 @@ __device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[3
         dense_block<2, false>(p, p.z, stg, p0, q0, lane);
         __syncwarp();
     }
-    if (p.act != MILO_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = dense_act(p.act, v[i]);
-    }
+    act_tile(p.act, v);
     if (p.residual) {
         if (p.y_dt == MILO_F32) dense_block<4, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
         else dense_block<2, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
@@ -203,25 +200,35 @@ __device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[3
 // Swapped form: the lane's row is feature p0 + lane, its N values tokens q0..:
 // y[q, p], consecutive lanes at consecutive addresses.
 template <int N>
-__device__ __forceinline__ void dense_store_swapped(const DenseTc& p, const float (&v)[N], int p0, int q0, int lane,
+__device__ __forceinline__ void dense_store_swapped(const DenseTc& p, float (&v)[N], int p0, int q0, int lane,
                                                     int32_t& st) {
     const int f = p0 + lane;
     if (f >= p.P) return;
-    const float b = p.bias ? load16(p.bias, f, p.bf16) : 0.0f;
+    if (p.bias) {
+        const float b = load16(p.bias, f, p.bf16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (q0 + i >= p.Q) break;
-        const size_t o = static_cast<size_t>(q0 + i) * p.P + f;
-        float t = v[i] + b;
-        if (p.z) static_cast<uint16_t*>(p.z)[o] = round16(t, p.bf16, st);
-        t = dense_act(p.act, t);
-        if (p.residual) t += load_any(p.residual, o, p.y_dt);
-        store_any(p.y, o, p.y_dt, t, st);
+        for (int i = 0; i < N; ++i) v[i] += b;
     }
+    const int n = min(N, p.Q - q0);
+    const size_t o = static_cast<size_t>(q0) * p.P + f;
+    if (p.z) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) static_cast<uint16_t*>(p.z)[o + static_cast<size_t>(i) * p.P] = round16(v[i], p.bf16, st);
+    }
+    act_tile(p.act, v);
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) v[i] += load_any(p.residual, o + static_cast<size_t>(i) * p.P, p.y_dt);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n) store_any(p.y, o + static_cast<size_t>(i) * p.P, p.y_dt, v[i], st);
 }
 
 template <bool SWAP>
-__global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(const __grid_constant__ DenseTc p) {
+__global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_constant__ DenseTc p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
@@ -460,6 +467,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 
 constexpr int kDtSmemMax = 227 * 1024 - 1024;     // less the slack that aligns the base
+constexpr int kDtSmemHalf = 113 * 1024 - 1024;    // two CTAs on an SM
 
 static int dense_sms() {
     int dev = 0, n = 148;
@@ -504,6 +512,7 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
 }
 
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
+    if (g.P <= kDenseFewRows && !g.a_mn && !g.b_mn) return launch_dense_few(g, what, s);
     DenseTc p;
     memset(&p, 0, sizeof(p));
     // few rows of A (tokens): they become the columns
@@ -532,13 +541,16 @@ milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t
     const long long tiles = static_cast<long long>(p.tiles_p) * p.tiles_q;
     if (tiles > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
     p.tiles = static_cast<int>(tiles);
+    // Split of c: as many CTAs as run at once (two per SM), each with at least
+    // four slices of c.
     p.split = 1;
-    while (p.split < kDtMaxSplit && p.tiles * p.split * 2 <= 2 * sms && p.kblocks >= 4 * p.split) p.split *= 2;
+    while (p.split < kDtMaxSplit && p.tiles * p.split * 2 <= 2 * sms && p.kblocks >= 8 * p.split) p.split *= 2;
     p.bufs = p.split == 1 && p.tiles > sms ? 2 : 1;
+    const int budget = p.tiles * p.split > sms && p.bufs == 1 ? kDtSmemHalf : kDtSmemMax;
     p.stage_bytes = kDtAtom + p.bn * 128;
     const int extra = 4 * kDtStaging + 4 * kDtBias * 4 + 512;
     const int kper = (p.kblocks + p.split - 1) / p.split;
-    p.stages = std::min({kDtMaxStages, (kDtSmemMax - extra) / p.stage_bytes, std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
+    p.stages = std::min({kDtMaxStages, (budget - extra) / p.stage_bytes, std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
     int ring = p.stages * p.stage_bytes;
     if (p.split > 1) ring = std::max(ring, p.bn * kDtRows * 4);
     p.off_staging = ring;

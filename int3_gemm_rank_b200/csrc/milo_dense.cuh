@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "milo_device.cuh"
 
 namespace milo {
@@ -26,39 +28,66 @@ struct DenseGemm {
     int32_t* dev_status;
 };
 
-__device__ __forceinline__ float dense_act(int act, float z) {
-    switch (act) {
-        case MILO_ACT_RELU: return z <= 0.0f ? 0.0f : z;     // NaN stays
-        case MILO_ACT_SILU: return z / (1.0f + expf(-z));
-        case MILO_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-        case MILO_ACT_GELU_TANH: {
-            // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), without the cancellation near -1
-            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-            return z / (1.0f + expf(-2.0f * u));
-        }
-        default: return z;
+// The activations in fp32, act by act so that a loop over a register tile has
+// no branch in it.  1 / (1 + exp(-v)) by the fast exponential and division:
+// relative error below 2^-21 + 2^-23 |v|, times v (1 - v / ...) <= 0.3 in the
+// result, so within 2^-20 (|z| + 1) of the function and far below the half
+// step of a 16-bit result.
+__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == MILO_ACT_RELU) {
+        return z <= 0.0f ? 0.0f : z;                             // NaN stays
+    } else if constexpr (ACT == MILO_ACT_SILU) {
+        return z * sigmoid_fast(z);
+    } else if constexpr (ACT == MILO_ACT_GELU) {
+        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    } else if constexpr (ACT == MILO_ACT_GELU_TANH) {
+        // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), without the cancellation near -1
+        return z * sigmoid_fast(z * fmaf(0.07135481627260f, z * z, 1.59576912160573f));
+    } else {
+        return z;
     }
 }
 
-__device__ __forceinline__ float dense_dact(int act, float z) {
-    switch (act) {
-        case MILO_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-        case MILO_ACT_SILU: {
-            const float g = 1.0f / (1.0f + expf(-z));
-            return g * (1.0f + z * (1.0f - g));
-        }
-        case MILO_ACT_GELU:
-            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-                   z * expf(-0.5f * z * z) * 0.39894228040143268f;
-        case MILO_ACT_GELU_TANH: {
-            // past |z| = 16 the slope is 0 or 1 to the last bit, and z^2 may overflow
-            if (fabsf(z) > 16.0f) return z > 0.0f ? 1.0f : 0.0f;
-            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-            const float g = 1.0f / (1.0f + expf(-2.0f * u));
-            return g + z * g * (1.0f - g) * 1.59576912160573071f * (1.0f + 0.134145f * z * z);
-        }
-        default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == MILO_ACT_RELU) {
+        return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    } else if constexpr (ACT == MILO_ACT_SILU) {
+        const float g = sigmoid_fast(z);
+        return g * fmaf(z, 1.0f - g, 1.0f);
+    } else if constexpr (ACT == MILO_ACT_GELU) {
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+    } else if constexpr (ACT == MILO_ACT_GELU_TANH) {
+        // past |z| = 16 the slope is 0 or 1 to the last bit, and z^2 may overflow
+        const float c = fminf(fmaxf(z, -16.0f), 16.0f);
+        const float g = sigmoid_fast(c * fmaf(0.07135481627260f, c * c, 1.59576912160573f));
+        return z == z ? fmaf(c * g * (1.0f - g), fmaf(0.21406444881780f, c * c, 1.59576912160573f), g) : z;
+    } else {
+        return 1.0f;
     }
+}
+
+// f(std::integral_constant<int, act>) for a run-time act.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    switch (act) {
+        case MILO_ACT_RELU: f(std::integral_constant<int, MILO_ACT_RELU>{}); break;
+        case MILO_ACT_SILU: f(std::integral_constant<int, MILO_ACT_SILU>{}); break;
+        case MILO_ACT_GELU: f(std::integral_constant<int, MILO_ACT_GELU>{}); break;
+        case MILO_ACT_GELU_TANH: f(std::integral_constant<int, MILO_ACT_GELU_TANH>{}); break;
+        default: f(std::integral_constant<int, MILO_ACT_NONE>{}); break;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void act_tile(int act, float (&v)[N]) {
+    with_act(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+    });
 }
 
 __device__ __forceinline__ float load16(const void* p, size_t i, int bf16) {
@@ -82,6 +111,10 @@ __device__ __forceinline__ void store_any(void* p, size_t i, int dt, float v, in
     else static_cast<uint16_t*>(p)[i] = round16(v, dt == MILO_BF16, st);
 }
 
-milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s);
+// Tokens up to which the forward product goes to the kernel for few rows.
+constexpr int kDenseFewRows = 16;
+
+milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s);       // dense_tc.cu
+milo_status launch_dense_few(const DenseGemm& g, const char* what, cudaStream_t s);        // dense_few.cu
 
 }  // namespace milo
