@@ -6,8 +6,9 @@
 // fp32), with no shared memory on the way.  A block owns 16 rows of W, its
 // warps share K in steps of 32; a lane's A fragments of two k16 steps are 16
 // contiguous bytes of two rows (the k order inside a step is free as long as x
-// uses the same), so W and x come by 16-byte loads, kFewSteps of them in
-// flight per operand and lane.  The warps' partial sums meet in shared memory
+// uses the same), so W and x come by 16-byte loads, S steps of them in flight
+// per lane: each step's registers are loaded anew as soon as its product is
+// issued.  The warps' partial sums meet in shared memory
 // in warp order.  (The tcgen05 tile of 16 columns, fed by TMA and split over a
 // cluster, took 26 us for 1 x 4096 x 4096 bf16.)
 #include <cuda_runtime.h>
@@ -18,7 +19,6 @@
 namespace milo {
 
 constexpr int kFewRows = 16;                // rows of W per block
-constexpr int kFewSteps = 4;                // k32 steps loaded ahead
 
 struct DenseFew {
     const uint16_t *x, *W;
@@ -41,6 +41,7 @@ __device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32
 // NT tiles of 8 tokens; WARPS warps share K.
 template <bool BF16, int NT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) dense_few_kernel(const DenseFew p) {
+    constexpr int S = NT == 1 ? 8 : 4;          // k32 steps in flight
     __shared__ float part[WARPS][NT * 8][kFewRows + 1];
     grid_dep_launch();
     grid_dep_wait();
@@ -63,19 +64,20 @@ __global__ void __launch_bounds__(32 * WARPS) dense_few_kernel(const DenseFew p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int k0 = 32 * warp; k0 < p.K; k0 += 32 * WARPS * kFewSteps) {
-        uint4 a[kFewSteps], b[kFewSteps], xv[kFewSteps][NT];
+    uint4 a[S], b[S], xv[S][NT];
+    auto load = [&](int s, int k) {
+        const bool in = k + 8 * c < p.K;                  // K is a multiple of 8
+        a[s] = in && r0 ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : zero;
+        b[s] = in && r1 ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : zero;
 #pragma unroll
-        for (int s = 0; s < kFewSteps; ++s) {
-            const int k = k0 + 32 * WARPS * s;
-            const bool in = k + 8 * c < p.K;              // K is a multiple of 8
-            a[s] = in && r0 ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : zero;
-            b[s] = in && r1 ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+        for (int t = 0; t < NT; ++t) xv[s][t] = in && xin[t] ? *reinterpret_cast<const uint4*>(xr[t] + k) : zero;
+    };
+    constexpr int kStep = 32 * WARPS;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) xv[s][t] = in && xin[t] ? *reinterpret_cast<const uint4*>(xr[t] + k) : zero;
-        }
+    for (int s = 0; s < S; ++s) load(s, 32 * warp + s * kStep);
+    for (int k0 = 32 * warp; k0 < p.K; k0 += S * kStep)
 #pragma unroll
-        for (int s = 0; s < kFewSteps; ++s)
+        for (int s = 0; s < S; ++s) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if constexpr (BF16) {
@@ -86,7 +88,8 @@ __global__ void __launch_bounds__(32 * WARPS) dense_few_kernel(const DenseFew p)
                     mma16816(acc[t], a[s].z, b[s].z, a[s].w, b[s].w, xv[s][t].z, xv[s][t].w);
                 }
             }
-    }
+            load(s, k0 + (S + s) * kStep);
+        }
     // acc[t][i]: W row g + 8 (i >> 1), token 8 t + 2 c + (i & 1)
 #pragma unroll
     for (int t = 0; t < NT; ++t)

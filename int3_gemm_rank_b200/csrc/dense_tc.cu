@@ -13,10 +13,11 @@
 //     they are stored by the forward product and by both gradients.
 //   - Many tiles: a persistent grid, two accumulators in TMEM, so that the
 //     epilogue of one tile runs under the products of the next.
-//   - Few tiles: c is split over the CTAs of a cluster.  Each leaves its
-//     partial tile in its shared memory; after a cluster barrier every warp
-//     of the cluster takes a share of the tile and adds the partials in rank
-//     order (no workspace, no atomics, the same bits every time).
+//   - Few tiles: c is split over the CTAs of a cluster.  The tile's blocks of
+//     32 rows by 32 (SWAP: 16) columns are dealt out to the CTAs; each sends its
+//     partial blocks to their owners' shared memory, and after a cluster
+//     barrier the owners add them in rank order (no workspace, no atomics, the
+//     same bits every time).
 //   - Few tokens: the operands change places (SWAP), the weight's rows fill
 //     the 128 rows of the tile and the tokens its BN columns, so one token
 //     costs a tile of 16 columns, not of 128 rows.
@@ -30,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "milo_dense.cuh"
 #include "milo_host.h"
@@ -71,16 +73,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// fp32 at the same shared-memory address of CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_peer(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Four floats to the same shared-memory address of CTA `rank` of the cluster.
+__device__ __forceinline__ void st_peer4(uint32_t saddr, uint32_t rank, float4 v) {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 // Matrix descriptor of an MN-major operand in the 128-byte swizzled layout:
@@ -239,9 +241,12 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = p.split > 1 ? cluster_rank() : 0u;
+    constexpr int W = SWAP ? 16 : kDtChunk;      // columns of a block of the split epilogue
 
     grid_dep_launch();
     if (threadIdx.x == 0) {
+        prefetch_map(&p.a_map);
+        prefetch_map(&p.b_map);
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -399,46 +404,62 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         }
     } else {
         // ---------------------------------------------------------------- epilogue, split over the cluster:
-        // this CTA's partial tile to its shared memory (the stages are done
-        // with: the accumulator's commit covers every MMA that read them)
+        // this CTA's partial blocks to their owners: block u (rows 32 (u % 4)..,
+        // columns W (u / 4)..) to warp u / split % 4 of CTA u % split, there at
+        // [u / split][rank], four columns of a lane's row together
         const int quarter = warp & 3;
         const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
-        float* part = reinterpret_cast<float*>(smem);
         if (!warp_wait(&afull[0], 0)) st_bits |= MILO_DEV_TIMEOUT;
         tc_fence_after();
-        for (int c = 0; c < p.bn; c += 16) {
-            uint32_t d[16];
-            tc_ld(lane_base + c, d);
+        __syncwarp();
+        cluster_arrive();        // this CTA is done with its ring ...
+        cluster_wait();          // ... and so are the others: the blocks go there
+        for (int c = 0; c < p.bn / W; ++c) {
+            const int u = 4 * c + quarter;
+            const uint32_t dst = smem_u32(smem) + (u / p.split * p.split + rank) * (W * 128) + lane * 16;
+            uint32_t d[W];
+            tc_ld(lane_base + W * c, d);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * kDtRows + 32 * quarter + lane] = __uint_as_float(d[i]);
+            for (int i = 0; i < W / 4; ++i)
+                st_peer4(dst + i * 512, u % p.split,
+                         make_float4(__uint_as_float(d[4 * i]), __uint_as_float(d[4 * i + 1]), __uint_as_float(d[4 * i + 2]),
+                                     __uint_as_float(d[4 * i + 3])));
         }
         tc_fence_before();
     }
 
     if (p.split > 1) {
         __syncwarp();
-        cluster_sync();
+        if (warp < 2) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        cluster_arrive();
+        cluster_wait();
         if (warp >= 2) {
-            // units of 32 rows by 16 (SWAP) or 32 columns, over the cluster's epilogue warps
             int tp, tq;
             dense_tile(p, first, tp, tq);
-            constexpr int W = SWAP ? 16 : kDtChunk;
             const int quarter = warp & 3;
             uint8_t* stg = smem + p.off_staging + quarter * kDtStaging;
             float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + quarter * kDtBias;
-            const uint32_t base = smem_u32(smem);
-            const int units = 4 * (p.bn / W);
-            for (int u = static_cast<int>(rank) * 4 + quarter; u < units; u += p.split * 4) {
-                const int r0 = 32 * (u & 3), c0 = W * (u >> 2);
-                const int p0 = tp * kDtRows + r0, q0 = tq * p.bn + c0;
+            for (int i = quarter; i * p.split + static_cast<int>(rank) < 4 * (p.bn / W); i += 4) {
+                const int u = i * p.split + static_cast<int>(rank);
+                const int p0 = tp * kDtRows + 32 * (u & 3), q0 = tq * p.bn + W * (u >> 2);
                 if (p0 >= p.P || q0 >= p.Q) continue;
+                const float4* src = reinterpret_cast<const float4*>(smem + i * p.split * (W * 128)) + lane;
                 float v[W];
 #pragma unroll
-                for (int i = 0; i < W; ++i) v[i] = 0.0f;
+                for (int j = 0; j < W; ++j) v[j] = 0.0f;
                 for (int s = 0; s < p.split; ++s)
 #pragma unroll
-                    for (int i = 0; i < W; ++i) v[i] += ld_peer(base + ((c0 + i) * kDtRows + r0 + lane) * 4, s);
+                    for (int j = 0; j < W / 4; ++j) {
+                        const float4 t = src[(s * (W / 4) + j) * 32];
+                        v[4 * j] += t.x;
+                        v[4 * j + 1] += t.y;
+                        v[4 * j + 2] += t.z;
+                        v[4 * j + 3] += t.w;
+                    }
                 if constexpr (SWAP) {
                     dense_store_swapped(p, v, p0, q0, lane, st_bits);
                 } else {
@@ -450,8 +471,6 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 }
             }
         }
-        __syncwarp();
-        cluster_sync();      // no CTA leaves while another still reads its partial tile
     }
     flag(p.dev_status, st_bits);
     tc_fence_before();
@@ -467,7 +486,6 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 
 constexpr int kDtSmemMax = 227 * 1024 - 1024;     // less the slack that aligns the base
-constexpr int kDtSmemHalf = 113 * 1024 - 1024;    // two CTAs on an SM
 
 static int dense_sms() {
     int dev = 0, n = 148;
@@ -511,6 +529,37 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
     return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP>, p);
 }
 
+// Columns of a tile and split of c, by an estimate in SM cycles of a CTA's
+// work: a slice of c takes bn * 2 cycles of the tensor core or its bytes at 90
+// bytes a cycle (what one SM was seen to draw from L2), whichever is longer; a
+// wave of tiles takes its slices and, when nothing follows to hide it, an
+// epilogue; all of it at least the operands' bytes at the measured copy rate
+// (3.4 bytes a cycle and SM each way, at 148 SMs and 1.9 GHz: 23 in all).
+static void dense_plan(DenseTc& p, bool swap, int sms) {
+    double best = -1.0;
+    const double dram = (static_cast<double>(p.P) + p.Q) * p.C * 2.0 / (23.0 * 148.0);
+    const int bn_swap = static_cast<int>(round_up(p.Q, 16));
+    for (int bn = swap ? bn_swap : 64; bn <= (swap ? bn_swap : 256); bn *= 2) {
+        if (!swap && bn > 64 && bn / 2 >= p.Q) break;            // the tile would be mostly empty
+        const double tiles = std::ceil(p.P / 128.0) * std::ceil(p.Q / static_cast<double>(bn));
+        const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 90.0);
+        for (int split = 1; split <= kDtMaxSplit && (split == 1 || p.kblocks >= 2 * split); split *= 2) {
+            const double waves = std::ceil(tiles * split / sms);
+            if (split > 1 && waves > 1.0) break;                 // clusters only where one wave holds them
+            const double epilogue = 8.0 * bn * (split > 1 ? 1.0 / split : 1.0);
+            const double cost = std::max(dram, waves * std::ceil(p.kblocks / static_cast<double>(split)) * slice) + epilogue +
+                                (split > 1 ? 1500.0 + 100.0 * split : 0.0);
+            if (best < 0.0 || cost < best) {
+                best = cost;
+                p.bn = bn;
+                p.split = split;
+            }
+        }
+    }
+    p.tiles_p = (p.P + kDtRows - 1) / kDtRows;
+    p.tiles_q = (p.Q + p.bn - 1) / p.bn;
+}
+
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
     if (g.P <= kDenseFewRows && !g.a_mn && !g.b_mn) return launch_dense_few(g, what, s);
     DenseTc p;
@@ -527,35 +576,24 @@ milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t
     const long long lda = swap ? g.ldb : g.lda, ldb = swap ? g.lda : g.ldb;
     p.bf16 = g.bf16;
     p.kblocks = (p.C + kDtK - 1) / kDtK;
-    p.tiles_p = (p.P + kDtRows - 1) / kDtRows;
     const int sms = dense_sms();
-    if (swap) {
-        p.bn = static_cast<int>(round_up(p.Q, 16));
-    } else {
-        p.bn = 256;
-        while (p.bn > 64 && (p.bn / 2 >= p.Q ||
-                             static_cast<long long>(p.tiles_p) * ((p.Q + p.bn - 1) / p.bn) < sms))
-            p.bn /= 2;
-    }
-    p.tiles_q = (p.Q + p.bn - 1) / p.bn;
+    dense_plan(p, swap, sms);
     const long long tiles = static_cast<long long>(p.tiles_p) * p.tiles_q;
     if (tiles > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
     p.tiles = static_cast<int>(tiles);
-    // Split of c: as many CTAs as run at once (two per SM), each with at least
-    // four slices of c.
-    p.split = 1;
-    while (p.split < kDtMaxSplit && p.tiles * p.split * 2 <= 2 * sms && p.kblocks >= 8 * p.split) p.split *= 2;
     p.bufs = p.split == 1 && p.tiles > sms ? 2 : 1;
-    const int budget = p.tiles * p.split > sms && p.bufs == 1 ? kDtSmemHalf : kDtSmemMax;
     p.stage_bytes = kDtAtom + p.bn * 128;
-    const int extra = 4 * kDtStaging + 4 * kDtBias * 4 + 512;
+    // shared memory: the ring (then a split's partial blocks), the row form's
+    // staging and bias, barriers
+    const int staging = swap ? 0 : 4 * kDtStaging, bias = swap ? 0 : 4 * kDtBias * 4;
+    const int w = swap ? 16 : kDtChunk;
+    const int part = p.split > 1 ? static_cast<int>(round_up(4 * (p.bn / w), p.split)) * w * 128 : 0;
     const int kper = (p.kblocks + p.split - 1) / p.split;
-    p.stages = std::min({kDtMaxStages, (budget - extra) / p.stage_bytes, std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
-    int ring = p.stages * p.stage_bytes;
-    if (p.split > 1) ring = std::max(ring, p.bn * kDtRows * 4);
-    p.off_staging = ring;
-    p.off_bias = p.off_staging + 4 * kDtStaging;
-    p.off_bar = p.off_bias + 4 * kDtBias * 4;
+    p.stages = std::min({kDtMaxStages, (kDtSmemMax - staging - bias - 512) / p.stage_bytes,
+                         std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
+    p.off_staging = std::max(p.stages * p.stage_bytes, part);
+    p.off_bias = p.off_staging + staging;
+    p.off_bar = p.off_bias + bias;
     const int smem = p.off_bar + 512 + 1024;
     p.tmem_cols = 32;
     while (p.tmem_cols < static_cast<uint32_t>(p.bufs * p.bn)) p.tmem_cols *= 2;

@@ -184,3 +184,26 @@ def test_binding_needs_cuda_tensors(milo):
         milo.milo_dense_linear(torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((16, 64), dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="contiguous CUDA"):
         milo.milo_dispatch(torch.zeros((4, 64), dtype=torch.bfloat16), _route(4, 2))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the made-up pointers below must not reach a GPU")
+def test_planning_of_extreme_sizes_returns(milo):
+    """Without a GPU the calls get as far as the driver: the host planning of
+    every size returns an error status, never a crash."""
+    import random
+    L, rng = milo.lib(), random.Random(1)
+    edge = [1, 2, 7, 8, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 4096, 65536, 1 << 24]
+    for i in range(600):
+        M, N, K = (rng.choice(edge) if rng.random() < 0.7 else rng.randint(1, 1 << 24) for _ in range(3))
+        K = max(8, K // 8 * 8)
+        dt, act = rng.randint(0, 1), rng.randint(0, 4)
+        ok = (milo.MILO_ERR_CUDA, milo.MILO_ERR_UNSUPPORTED_SHAPE)
+        assert _linear(L, dt=dt, M=M, N=N, K=K, act=act, bias=F, ydt=rng.randint(0, 2)) in ok, (M, N, K)
+        assert _backward(L, dt=dt, M=M, N=N, K=K, act=act, z=F, n=1 << 62) in ok, (M, N, K)
+        T, k, H, E = rng.choice(edge), rng.randint(1, 16), rng.choice(edge), rng.randint(1, 256)
+        w = rng.choice([None, F])
+        assert L.milo_dispatch(F, dt, T, k, H, F, w, F, dt, None, None) in ok
+        assert L.milo_combine(F, dt, T, k, H, F, w, rng.choice([None, F]), F, rng.randint(0, 2), None, None) in ok
+        assert L.milo_dispatch_backward(F, dt, T, k, H, F, F, F, F, dt, F, None, None) in ok
+        assert L.milo_combine_backward(F, dt, T, k, H, F, F, F, F, dt, F, None, None) in ok
+        assert L.milo_route_backward(F, F, F, F, T, E, min(k, E), dt, F, 2, None, None) in ok
