@@ -6,7 +6,7 @@
 //   - A work item is a 128 x BN tile of D.  One warp brings 64-deep slices of A
 //     and B by 2-D TMA (128-byte swizzle) into a ring of stages, one warp
 //     issues tcgen05.mma (M = 128, N = BN, K = 16, fp32 accumulator in TMEM),
-//     four warps turn the finished accumulator into output.
+//     eight warps turn the finished accumulator into output.
 //   - Either operand may lie along c (K-major: a box of 64 c by 128 rows) or
 //     along its rows (MN-major: boxes of 64 rows by 64 c); only the boxes'
 //     coordinates and the matrix descriptors differ, so W and x are read as
@@ -43,13 +43,17 @@ constexpr int kDtRows = 128;                 // rows of A in a tile (MMA M)
 constexpr int kDtK = 64;                     // c per stage: one 128-byte swizzled row
 constexpr int kDtAtom = kDtRows * kDtK * 2;  // bytes of an A stage
 constexpr int kDtBox = 64 * kDtK * 2;        // bytes of an MN-major box (64 rows x 64 c)
-constexpr int kDtThreads = 192;              // producer, MMA, four epilogue warps
+constexpr int kDtEpiWarps = 8;               // two per TMEM lane quarter, every other block of columns each
+constexpr int kDtThreads = 32 * (2 + kDtEpiWarps);   // producer, MMA, epilogue
 constexpr int kDtMaxStages = 12;
 constexpr int kDtMaxSplit = 8;               // portable cluster size
-constexpr int kDtPitch = 144;                // bytes between rows of the output staging (32 fp32, padded)
-constexpr int kDtStaging = 32 * kDtPitch;    // per epilogue warp
-constexpr int kDtBias = 256;                 // fp32 bias columns, per epilogue warp
 constexpr int kDtChunk = 32;                 // accumulator columns handled at a time
+constexpr int kDtBias = 128;                 // fp32 bias columns, per epilogue warp (its half of 256)
+
+// Output staging of an epilogue warp: 32 rows of 32 elements, 16 bytes apart
+// from a multiple of 128 so that 16-byte pieces of a column fall on different
+// banks.
+constexpr int dense_pitch(int esize) { return 32 * esize + 16; }
 
 struct DenseTc {
     CUtensorMap a_map, b_map;
@@ -59,7 +63,7 @@ struct DenseTc {
     int tiles_p, tiles_q, tiles;
     uint32_t idesc, tmem_cols;
     int bufs;                                // accumulators in TMEM (2: persistent)
-    int stage_bytes, off_staging, off_bias, off_bar;
+    int stage_bytes, staging, off_staging, off_bias, off_bar;
     int vec;                                 // 16-byte output rows
     // epilogue (y, residual and z are [M, N]; SWAP: p is the feature)
     const void *bias, *residual;
@@ -114,89 +118,121 @@ __device__ __forceinline__ void dense_tile(const DenseTc& p, int item, int& tp, 
 // y[p, q].  v holds the lane's row.  st32 is the warp's staging buffer.
 // ---------------------------------------------------------------------------
 
-// The warp's 32 x 32 block between staging rows (kDtPitch apart) and global
-// rows p0.., columns q0..; E bytes an element.  16-byte pieces when p.vec.
-template <int E, bool LOAD>
+// The warp's 32 x 32 block between staging rows and global rows p0.., columns
+// q0..; 16-byte pieces when p.vec.
+template <int DT, bool LOAD>
 __device__ __forceinline__ void dense_block(const DenseTc& p, void* g, uint8_t* stg, int p0, int q0, int lane) {
+    constexpr int E = DT == MILO_F32 ? 4 : 2, kPitch = dense_pitch(E);
     constexpr int kPieces = 32 * E / 16;              // 16-byte pieces of a row
     constexpr int kRows = 32 / kPieces;               // rows of one pass
     if (p.vec) {
         const int piece = lane % kPieces, r0 = lane / kPieces;
         const bool in = q0 + piece * (16 / E) < p.Q;  // Q is a multiple of a piece here
+        uint8_t* gp = static_cast<uint8_t*>(g) + (static_cast<size_t>(p0 + r0) * p.Q + q0) * E + piece * 16;
+        uint4 t[32 / kRows];
 #pragma unroll
         for (int i = 0; i < 32 / kRows; ++i) {
-            const int r = r0 + i * kRows;
-            if (in && p0 + r < p.P) {
-                uint4* gp = reinterpret_cast<uint4*>(static_cast<uint8_t*>(g) +
-                                                     (static_cast<size_t>(p0 + r) * p.Q + q0) * E) + piece;
-                uint4* sp = reinterpret_cast<uint4*>(stg + r * kDtPitch) + piece;
-                if constexpr (LOAD) *sp = *gp;
-                else *gp = *sp;
+            if constexpr (LOAD) {
+                if (in && p0 + r0 + i * kRows < p.P) t[i] = *reinterpret_cast<const uint4*>(gp + static_cast<size_t>(i) * kRows * p.Q * E);
+            } else {
+                t[i] = *reinterpret_cast<const uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+            if constexpr (LOAD) {
+                *reinterpret_cast<uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16) = t[i];
+            } else {
+                if (in && p0 + r0 + i * kRows < p.P) *reinterpret_cast<uint4*>(gp + static_cast<size_t>(i) * kRows * p.Q * E) = t[i];
             }
         }
     } else {
         using T = typename std::conditional<E == 4, uint32_t, uint16_t>::type;
-        if (q0 + lane < p.Q)
-            for (int r = 0; r < 32 && p0 + r < p.P; ++r) {
-                T* gp = static_cast<T*>(g) + static_cast<size_t>(p0 + r) * p.Q + q0 + lane;
-                T* sp = reinterpret_cast<T*>(stg + r * kDtPitch) + lane;
-                if constexpr (LOAD) *sp = *gp;
-                else *gp = *sp;
+        if (q0 + lane < p.Q) {
+            T* gp = static_cast<T*>(g) + static_cast<size_t>(p0) * p.Q + q0 + lane;
+            T* sp = reinterpret_cast<T*>(stg) + lane;
+            const int n = min(32, p.P - p0);
+#pragma unroll 8
+            for (int r = 0; r < n; ++r) {
+                if constexpr (LOAD) sp[r * (kPitch / E)] = gp[static_cast<size_t>(r) * p.Q];
+                else gp[static_cast<size_t>(r) * p.Q] = sp[r * (kPitch / E)];
             }
+        }
     }
 }
 
-// The lane's staging row <-> 32 values, as fp32 (F32) or 16-bit.
-__device__ __forceinline__ void stage_put(uint8_t* row, const float (&v)[32], int dt, int32_t& st) {
-    if (dt == MILO_F32) {
+// The lane's 32 values to its staging row, and the block to global memory.
+template <int DT>
+__device__ __forceinline__ void dense_put(const DenseTc& p, void* g, const float (&v)[32], uint8_t* stg, int p0, int q0,
+                                          int lane, int32_t& st) {
+    uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
+    if constexpr (DT == MILO_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             reinterpret_cast<float4*>(row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack16<DT>(v[2 * i], v[2 * i + 1]);
+        if constexpr (DT == MILO_F16) half_range(v, w, st);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(row)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __syncwarp();
+    dense_block<DT, false>(p, g, stg, p0, q0, lane);
+    __syncwarp();
+}
+
+// v += the block of the residual.
+template <int DT>
+__device__ __forceinline__ void dense_add(const DenseTc& p, float (&v)[32], uint8_t* stg, int p0, int q0, int lane) {
+    dense_block<DT, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
+    __syncwarp();
+    const uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
+    if constexpr (DT == MILO_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 t = reinterpret_cast<const float4*>(row)[i];
+            v[4 * i] += t.x;
+            v[4 * i + 1] += t.y;
+            v[4 * i + 2] += t.z;
+            v[4 * i + 3] += t.w;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            const uint4 t = reinterpret_cast<const uint4*>(row)[i];
+            const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[q] = static_cast<uint32_t>(round16(v[8 * i + 2 * q], dt == MILO_BF16, st)) |
-                       (static_cast<uint32_t>(round16(v[8 * i + 2 * q + 1], dt == MILO_BF16, st)) << 16);
-            reinterpret_cast<uint4*>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int q = 0; q < 8; ++q) v[8 * i + q] += unpack16<DT>(w[q / 2], q & 1);
         }
     }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[32], uint8_t* stg, const float* bias,
                                                   int p0, int q0, int lane, int32_t& st) {
-    uint8_t* row = stg + lane * kDtPitch;
     if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += bias[i];
+        for (int i = 0; i < 8; ++i) {
+            const float4 t = reinterpret_cast<const float4*>(bias)[i];
+            v[4 * i] += t.x;
+            v[4 * i + 1] += t.y;
+            v[4 * i + 2] += t.z;
+            v[4 * i + 3] += t.w;
+        }
     }
     if (p.z) {
-        stage_put(row, v, p.bf16 ? MILO_BF16 : MILO_F16, st);
-        __syncwarp();
-        dense_block<2, false>(p, p.z, stg, p0, q0, lane);
-        __syncwarp();
+        if (p.bf16) dense_put<MILO_BF16>(p, p.z, v, stg, p0, q0, lane, st);
+        else dense_put<MILO_F16>(p, p.z, v, stg, p0, q0, lane, st);
     }
     act_tile(p.act, v);
-    if (p.residual) {
-        if (p.y_dt == MILO_F32) dense_block<4, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
-        else dense_block<2, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
-        __syncwarp();
-        if (p.y_dt == MILO_F32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += reinterpret_cast<const float*>(row)[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += act_f32(reinterpret_cast<const uint16_t*>(row)[i], p.y_dt == MILO_BF16);
-        }
-        __syncwarp();
-    }
-    stage_put(row, v, p.y_dt, st);
-    __syncwarp();
-    if (p.y_dt == MILO_F32) dense_block<4, false>(p, p.y, stg, p0, q0, lane);
-    else dense_block<2, false>(p, p.y, stg, p0, q0, lane);
-    __syncwarp();
+    with_dtype(p.y_dt, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (p.residual) dense_add<DT>(p, v, stg, p0, q0, lane);
+        dense_put<DT>(p, p.y, v, stg, p0, q0, lane, st);
+    });
 }
 
 // Swapped form: the lane's row is feature p0 + lane, its N values tokens q0..:
@@ -213,20 +249,26 @@ __device__ __forceinline__ void dense_store_swapped(const DenseTc& p, float (&v)
     }
     const int n = min(N, p.Q - q0);
     const size_t o = static_cast<size_t>(q0) * p.P + f;
-    if (p.z) {
+    if (p.z)
+        with_dtype(p.bf16 ? MILO_BF16 : MILO_F16, [&](auto dt) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < n) static_cast<uint16_t*>(p.z)[o + static_cast<size_t>(i) * p.P] = round16(v[i], p.bf16, st);
-    }
+            for (int i = 0; i < N; ++i)
+                if (i < n) elem_store<decltype(dt)::value>(p.z, o + static_cast<size_t>(i) * p.P, v[i], st);
+        });
     act_tile(p.act, v);
-    if (p.residual) {
+    with_dtype(p.y_dt, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (p.residual) {
+            float r[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = i < n ? elem_load<DT>(p.residual, o + static_cast<size_t>(i) * p.P) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += r[i];
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < n) v[i] += load_any(p.residual, o + static_cast<size_t>(i) * p.P, p.y_dt);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) store_any(p.y, o + static_cast<size_t>(i) * p.P, p.y_dt, v[i], st);
+            if (i < n) elem_store<DT>(p.y, o + static_cast<size_t>(i) * p.P, v[i], st);
+    });
 }
 
 template <bool SWAP>
@@ -244,34 +286,48 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     constexpr int W = SWAP ? 16 : kDtChunk;      // columns of a block of the split epilogue
 
     grid_dep_launch();
-    if (threadIdx.x == 0) {
-        prefetch_map(&p.a_map);
-        prefetch_map(&p.b_map);
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    if (warp == 0) {
+        if (elect_one()) {
+            prefetch_map(&p.a_map);
+            prefetch_map(&p.b_map);
+            for (int s = 0; s < p.stages; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&afull[b], 1);
+                mbar_init(&aempty[b], kDtEpiWarps);
+            }
+            mbar_init(done_bar, 1);
+            fence_barrier_init();
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 4);
-        }
-        mbar_init(done_bar, 1);
-        fence_barrier_init();
+        __syncwarp();
     }
     // TMEM only once the kernels before have left: a CTA that held columns while
-    // it waits for them could keep one of their CTAs from its own
+    // it waits for them could keep one of their CTAs from its own.  The producer
+    // does not wait for it.
     grid_dep_wait();
-    if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tbase = *tmem_slot;
+    uint32_t tbase = 0;
+    if (warp == 0) {
+        asm volatile("bar.arrive 1, %0;" ::"n"(kDtThreads) : "memory");
+    } else {
+        if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
+        tc_fence_before();
+        named_sync(1, kDtThreads);
+        tc_fence_after();
+        tbase = *tmem_slot;
+    }
 
     // this CTA's share of c (all of it without a split)
     const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * rank / p.split);
     const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / p.split);
     const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
     int32_t st_bits = 0;
+    // epilogue warps: lane quarter, which half of the column blocks, own buffers
+    const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+    const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
+    uint8_t* stg = smem + p.off_staging + ew * p.staging;
+    float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + ew * kDtBias;
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -353,10 +409,6 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         if (!warp_wait(done_bar, 0)) st_bits |= MILO_DEV_TIMEOUT;
     } else if (p.split == 1) {
         // ---------------------------------------------------------------- epilogue, whole tiles
-        const int quarter = warp & 3;
-        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
-        uint8_t* stg = smem + p.off_staging + quarter * kDtStaging;
-        float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + quarter * kDtBias;   // the warp's own copy
         int buf = 0;
         uint32_t bph = 0;
         for (int it = first; it < p.tiles; it += step) {
@@ -365,8 +417,11 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             const int p0 = tp * kDtRows + 32 * quarter, q0 = tq * p.bn;
             if constexpr (!SWAP) {
                 if (p.bias) {
-                    for (int i = lane; i < p.bn; i += 32)
-                        sbias[i] = q0 + i < p.Q ? load16(p.bias, q0 + i, p.bf16) : 0.0f;
+                    // the columns of this warp's blocks, block after block
+                    for (int i = lane; i < p.bn / 2; i += 32) {
+                        const int q = q0 + (i / 32 * 2 + half) * 32 + lane;
+                        sbias[i] = q < p.Q ? load16(p.bias, q, p.bf16) : 0.0f;
+                    }
                     __syncwarp();
                 }
             }
@@ -376,26 +431,16 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             }
             tc_fence_after();
             const uint32_t acc = lane_base + static_cast<uint32_t>(buf * p.bn);
-            if constexpr (SWAP) {
-                for (int c = 0; c < p.bn; c += 16) {
-                    uint32_t d[16];
-                    tc_ld(acc + c, d);
-                    tc_wait_ld();
-                    float v[16];
+            for (int c = W * half; c < p.bn; c += 2 * W) {
+                uint32_t d[W];
+                tc_ld(acc + c, d);
+                tc_wait_ld();
+                float v[W];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(d[i]);
-                    dense_store_swapped(p, v, p0, q0 + c, lane, st_bits);
-                }
-            } else {
-                for (int c = 0; c < p.bn; c += kDtChunk) {
-                    uint32_t d[32];
-                    tc_ld(acc + c, d);
-                    tc_wait_ld();
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
-                    if (p0 < p.P && q0 + c < p.Q) dense_store_chunk(p, v, stg, sbias + c, p0, q0 + c, lane, st_bits);
-                }
+                for (int i = 0; i < W; ++i) v[i] = __uint_as_float(d[i]);
+                if (p0 >= p.P || q0 + c >= p.Q) continue;
+                if constexpr (SWAP) dense_store_swapped(p, v, p0, q0 + c, lane, st_bits);
+                else dense_store_chunk(p, v, stg, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
             }
             tc_fence_before();
             __syncwarp();
@@ -405,16 +450,14 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     } else {
         // ---------------------------------------------------------------- epilogue, split over the cluster:
         // this CTA's partial blocks to their owners: block u (rows 32 (u % 4)..,
-        // columns W (u / 4)..) to warp u / split % 4 of CTA u % split, there at
-        // [u / split][rank], four columns of a lane's row together
-        const int quarter = warp & 3;
-        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
+        // columns W (u / 4)..) to CTA u % split, there at [u / split][rank], four
+        // columns of a lane's row together
         if (!warp_wait(&afull[0], 0)) st_bits |= MILO_DEV_TIMEOUT;
         tc_fence_after();
         __syncwarp();
         cluster_arrive();        // this CTA is done with its ring ...
         cluster_wait();          // ... and so are the others: the blocks go there
-        for (int c = 0; c < p.bn / W; ++c) {
+        for (int c = half; c < p.bn / W; c += 2) {
             const int u = 4 * c + quarter;
             const uint32_t dst = smem_u32(smem) + (u / p.split * p.split + rank) * (W * 128) + lane * 16;
             uint32_t d[W];
@@ -440,10 +483,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         if (warp >= 2) {
             int tp, tq;
             dense_tile(p, first, tp, tq);
-            const int quarter = warp & 3;
-            uint8_t* stg = smem + p.off_staging + quarter * kDtStaging;
-            float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + quarter * kDtBias;
-            for (int i = quarter; i * p.split + static_cast<int>(rank) < 4 * (p.bn / W); i += 4) {
+            for (int i = ew; i * p.split + static_cast<int>(rank) < 4 * (p.bn / W); i += kDtEpiWarps) {
                 const int u = i * p.split + static_cast<int>(rank);
                 const int p0 = tp * kDtRows + 32 * (u & 3), q0 = tq * p.bn + W * (u >> 2);
                 if (p0 >= p.P || q0 >= p.Q) continue;
@@ -585,7 +625,8 @@ milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t
     p.stage_bytes = kDtAtom + p.bn * 128;
     // shared memory: the ring (then a split's partial blocks), the row form's
     // staging and bias, barriers
-    const int staging = swap ? 0 : 4 * kDtStaging, bias = swap ? 0 : 4 * kDtBias * 4;
+    p.staging = swap ? 0 : 32 * dense_pitch(g.y_dt == MILO_F32 ? 4 : 2);
+    const int staging = kDtEpiWarps * p.staging, bias = swap ? 0 : kDtEpiWarps * kDtBias * 4;
     const int w = swap ? 16 : kDtChunk;
     const int part = p.split > 1 ? static_cast<int>(round_up(4 * (p.bn / w), p.split)) * w * 128 : 0;
     const int kper = (p.kblocks + p.split - 1) / p.split;

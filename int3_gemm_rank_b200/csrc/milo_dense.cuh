@@ -82,6 +82,66 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     }
 }
 
+// f(std::integral_constant<int, dt>) for a run-time dtype: the loops inside have
+// no branch on it.
+template <typename F>
+__device__ __forceinline__ void with_dtype(int dt, F&& f) {
+    if (dt == MILO_BF16) f(std::integral_constant<int, MILO_BF16>{});
+    else if (dt == MILO_F16) f(std::integral_constant<int, MILO_F16>{});
+    else f(std::integral_constant<int, MILO_F32>{});
+}
+
+// Two fp32 values rounded to fp16 or bf16, as one word.
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (DT == MILO_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// FP16_RANGE for N values and their packed halves: one whose exponent field is
+// all ones (adding one there carries into the sign's place) is looked at again,
+// since an infinity may have been one before.
+template <int N>
+__device__ __forceinline__ void half_range(const float (&v)[N], const uint32_t* w, int32_t& st) {
+    uint32_t e = 0;
+#pragma unroll
+    for (int q = 0; q < N / 2; ++q) e |= (w[q] & 0x7C007C00u) + 0x04000400u;
+    if (e & 0x80008000u) {
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            if (fabsf(v[q]) >= 65520.0f && !isinf(v[q])) st |= MILO_DEV_FP16_RANGE;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float unpack16(uint32_t w, int hi) {
+    if constexpr (DT == MILO_BF16) return __uint_as_float(hi ? w & 0xFFFF0000u : w << 16);
+    else return __half2float(__ushort_as_half(static_cast<uint16_t>(hi ? w >> 16 : w & 0xFFFFu)));
+}
+
+// One element of a tensor of type DT.
+template <int DT>
+__device__ __forceinline__ float elem_load(const void* p, size_t i) {
+    if constexpr (DT == MILO_F32) return static_cast<const float*>(p)[i];
+    else return unpack16<DT>(static_cast<const uint16_t*>(p)[i], 0);
+}
+template <int DT>
+__device__ __forceinline__ void elem_store(void* p, size_t i, float v, int32_t& st) {
+    if constexpr (DT == MILO_F32) {
+        static_cast<float*>(p)[i] = v;
+    } else if constexpr (DT == MILO_BF16) {
+        static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    } else {
+        static_cast<uint16_t*>(p)[i] = __half_as_ushort(__float2half_rn(v));
+        if (fabsf(v) >= 65520.0f && !isinf(v)) st |= MILO_DEV_FP16_RANGE;
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void act_tile(int act, float (&v)[N]) {
     with_act(act, [&](auto a) {
