@@ -542,8 +542,8 @@ def _launch(dev, name: str, *args):
 
 def _need(t, name: str, dtypes, shape: tuple, device):
     """_arg with its checks in one expression for a tensor that passes them."""
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device and
-            t.is_cuda and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and
+            t.get_device() == device.index and t.is_contiguous()):
         _arg(t, name, dtypes, shape=shape, device=device)
 
 
@@ -552,7 +552,7 @@ def _out(t, name: str, shape: tuple, dtype, device):
     if t is None:
         if dtype not in _OUT:
             raise ValueError(f"{name} must be {' or '.join(_dname(d) for d in _OUT)}, not {_dname(dtype)}")
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     _need(t, name, _OUT, shape, device)
     return t
 
@@ -572,10 +572,13 @@ def _rows(t, name: str, rows: int, H: int | None, dtype, dev) -> int:
     """Checks rows [rows, H] on `dev` (any H and type when not given); returns H."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
-    if t.dim() != 2 or t.shape[0] != rows or (H is not None and t.shape[1] != H):
-        raise ValueError(f"{name} must be [{rows}, {'H' if H is None else H}], not {tuple(t.shape)}")
-    _need(t, name, _OUT if dtype is None else (dtype,), t.shape, dev)
-    return t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or (H is not None and shape[1] != H):
+        raise ValueError(f"{name} must be [{rows}, {'H' if H is None else H}], not {tuple(shape)}")
+    if (t.dtype not in _OUT or (dtype is not None and t.dtype is not dtype) or t.get_device() != dev.index or
+            not t.is_contiguous()):
+        _arg(t, name, _OUT if dtype is None else (dtype,), device=dev)
+    return shape[1]
 
 
 def _weights(w, T: int, k: int, dev):
@@ -665,7 +668,7 @@ def milo_combine_backward(dy: torch.Tensor, route: dict, ys: torch.Tensor | None
 
 def _grad_w(dw, T: int, k: int, dev):
     if dw is None:
-        return torch.empty((T, k), dtype=torch.float32, device=dev)
+        return torch.empty(T, k, dtype=torch.float32, device=dev)
     _need(dw, "dw", (torch.float32,), (T, k), dev)
     return dw
 
@@ -683,13 +686,15 @@ def _dense_args(x, W, act: str) -> tuple:
     device and the activation's code."""
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a [N, K] tensor")
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != W.shape[1]:
-        raise ValueError(f"x must be [M, {W.shape[1]}]")
+    N, K = W.shape
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [M, {K}]")
+    dev = x.device
     _arg(x, "x", _ACT)
-    _arg(W, "W", (x.dtype,), device=x.device)
+    _need(W, "W", (x.dtype,), (N, K), dev)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}, not {act!r}")
-    return x.shape[0], W.shape[0], x.shape[1], x.device, _ACTS[act]
+    return x.shape[0], N, K, dev, _ACTS[act]
 
 
 def milo_dense_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -744,7 +749,7 @@ def milo_dense_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tenso
             raise ValueError(f"need holds {name!r}; it may hold dx, dW and db")
         t = out.get(name) if out else None
         if t is None:
-            t = torch.empty(shapes[name], dtype=x.dtype, device=dev)
+            t = torch.empty(*shapes[name], dtype=x.dtype, device=dev)
         else:
             _arg(t, name, (x.dtype,), shape=shapes[name], device=dev)
         grads[name] = t
