@@ -23,9 +23,8 @@ namespace milo {
 // ---------------------------------------------------------------------------
 // dz = dy act'(z), and its column sums
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 64;         // rows of a block
 constexpr int kDzCols = 256;        // columns of a block
-constexpr int kDzThreads = 256;     // 32 groups of eight columns by 8 row lanes
+constexpr int kDzThreads = 256;     // 32 column lanes by 8 row lanes
 
 struct DzParams {
     const void* dy;             // [M, N] in dy_dt
@@ -34,99 +33,142 @@ struct DzParams {
     float* part;                // [row blocks][N] column sums, or NULL
     int32_t* dev_status;
     int M, N, ldz, dy_dt, bf16, act;
-    int vec;                    // dy and z in whole 16-byte pieces
-    int col_blocks;
+    int rows, col_blocks;       // rows of a block; blocks of columns
 };
 
-// Eight columns n.. of row m: 16-byte loads where rows allow them.
-__device__ __forceinline__ void dz_load8(const void* p, size_t row, int N, int n, int dt, int vec, float (&v)[8]) {
-    const size_t i = row * N + n;
-    if (vec && n < N) {
-        if (dt == MILO_F32) {
-            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-            const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// A lane's eight columns of a row of 256 that starts at column n0: VEC (dy and z
+// in whole 16-byte pieces) n0 + 8 lane.., else n0 + lane, + 32, ...
+template <int DT, bool VEC>
+__device__ __forceinline__ void dz_load(const void* p, size_t row, int N, int n0, int lane, float (&v)[8]) {
+    const size_t i = row * N + n0;
+    if constexpr (VEC) {
+        if (n0 + 8 * lane < N) {
+            if constexpr (DT == MILO_F32) {
+                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 8 * lane);
+                const float4 a = q[0], b = q[1];
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            } else {
+                const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i + 8 * lane);
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                v[q] = act_f32(static_cast<uint16_t>(q & 1 ? w[q / 2] >> 16 : w[q / 2] & 0xFFFFu), dt == MILO_BF16);
+                for (int q = 0; q < 8; ++q) v[q] = unpack16<DT>(w[q / 2], q & 1);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = 0.0f;
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = n + q < N ? load_any(p, i + q, dt) : 0.0f;
+        for (int q = 0; q < 8; ++q) v[q] = n0 + lane + 32 * q < N ? elem_load<DT>(p, i + lane + 32 * q) : 0.0f;
     }
 }
 
-// One block: kDzRows rows of 256 columns.  A thread takes eight columns of
-// every eighth row; the column sums of its rows are its own, and the eight row
-// lanes meet in shared memory in lane order.  Bound by memory: dy and z read,
-// dz written once.
+// One block: p.rows rows of 256 columns; a row lane takes every eighth row, four
+// of them in flight.  The column sums of a thread's rows are its own, and the
+// eight row lanes meet in shared memory in lane order.  Bound by memory: dy
+// and z read, dz written once.
+template <int DYT, int ZT, bool VEC, int ACT>
 __global__ void __launch_bounds__(kDzThreads) dense_dz_kernel(const DzParams p) {
+    constexpr int U = 4;
     __shared__ float red[8][kDzCols];
     grid_dep_launch();
     grid_dep_wait();
-    const int col = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int rb = static_cast<int>(blockIdx.x) / p.col_blocks, cb = static_cast<int>(blockIdx.x) % p.col_blocks;
-    const int n = cb * kDzCols + col;
-    const int m1 = min(p.M, (rb + 1) * kDzRows);
+    const int n0 = cb * kDzCols;
+    const int m0 = rb * p.rows, m1 = min(p.M, m0 + p.rows);
     int32_t st = 0;
     float sum[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
-    if (n < p.ldz) {
-        with_act(p.act, [&](auto act) {
-            constexpr int A = decltype(act)::value;
-#pragma unroll 2
-            for (int m = rb * kDzRows + rl; m < m1; m += 8) {
-                float v[8];
-                dz_load8(p.dy, m, p.N, n, p.dy_dt, p.vec, v);
-                if constexpr (A != MILO_ACT_NONE) {
-                    float z[8];
-                    dz_load8(p.z, m, p.N, n, p.bf16 ? MILO_BF16 : MILO_F16, p.vec, z);
+    for (int mb = m0 + rl; mb < m1; mb += 8 * U) {
+        float v[U][8], z[U][8];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] *= act_slope<A>(z[q]);
+        for (int u = 0; u < U; ++u)
+            if (mb + 8 * u < m1) {
+                dz_load<DYT, VEC>(p.dy, mb + 8 * u, p.N, n0, lane, v[u]);
+                if constexpr (ACT != MILO_ACT_NONE) dz_load<ZT, VEC>(p.z, mb + 8 * u, p.N, n0, lane, z[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (mb + 8 * u < m1) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if constexpr (ACT != MILO_ACT_NONE) v[u][q] *= act_slope<ACT>(z[u][q]);
+                    sum[q] += v[u][q];
                 }
-#pragma unroll
-                for (int q = 0; q < 8; ++q) sum[q] += v[q];
                 if (p.dz) {
+                    uint16_t* d = static_cast<uint16_t*>(p.dz) + static_cast<size_t>(mb + 8 * u) * p.ldz + n0;
                     uint32_t w[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = static_cast<uint32_t>(round16(v[2 * q], p.bf16, st)) |
-                               (static_cast<uint32_t>(round16(v[2 * q + 1], p.bf16, st)) << 16);
-                    // the scratch rows are whole 16-byte pieces
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + static_cast<size_t>(m) * p.ldz + n) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int q = 0; q < 4; ++q) w[q] = pack16<ZT>(v[u][2 * q], v[u][2 * q + 1]);
+                    if constexpr (ZT == MILO_F16) half_range(v[u], w, st);
+                    if constexpr (VEC) {
+                        if (n0 + 8 * lane < p.ldz) *reinterpret_cast<uint4*>(d + 8 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (n0 + lane + 32 * q < p.ldz)
+                                d[lane + 32 * q] = static_cast<uint16_t>(q & 1 ? w[q / 2] >> 16 : w[q / 2] & 0xFFFFu);
+                    }
                 }
             }
-        });
     }
     if (p.part) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) red[rl][col + q] = sum[q];
+        for (int q = 0; q < 8; ++q) red[rl][VEC ? 8 * lane + q : lane + 32 * q] = sum[q];
         __syncthreads();
-        const int nc = cb * kDzCols + threadIdx.x;
+        const int n = n0 + threadIdx.x;
         float s = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) s += red[q][threadIdx.x];
-        if (nc < p.N) p.part[static_cast<size_t>(rb) * p.N + nc] = s;
+        if (n < p.N) p.part[static_cast<size_t>(rb) * p.N + n] = s;
     }
     flag(p.dev_status, st);
 }
 
-// db[n] = the row blocks' sums, in order.
+template <int DYT, int ZT, bool VEC>
+static cudaError_t run_dz_act(const DzParams& p, int grid, cudaStream_t s) {
+    void (*k)(DzParams) = dense_dz_kernel<DYT, ZT, VEC, MILO_ACT_NONE>;
+    if (p.act == MILO_ACT_RELU) k = dense_dz_kernel<DYT, ZT, VEC, MILO_ACT_RELU>;
+    else if (p.act == MILO_ACT_SILU) k = dense_dz_kernel<DYT, ZT, VEC, MILO_ACT_SILU>;
+    else if (p.act == MILO_ACT_GELU) k = dense_dz_kernel<DYT, ZT, VEC, MILO_ACT_GELU>;
+    else if (p.act == MILO_ACT_GELU_TANH) k = dense_dz_kernel<DYT, ZT, VEC, MILO_ACT_GELU_TANH>;
+    return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kDzThreads), 0, s, p);
+}
+
+template <int DYT, int ZT>
+static cudaError_t run_dz_vec(const DzParams& p, bool vec, int grid, cudaStream_t s) {
+    return vec ? run_dz_act<DYT, ZT, true>(p, grid, s) : run_dz_act<DYT, ZT, false>(p, grid, s);
+}
+
+template <int ZT>
+static cudaError_t run_dz(const DzParams& p, bool vec, int grid, cudaStream_t s) {
+    if (p.dy_dt == MILO_F32) return run_dz_vec<MILO_F32, ZT>(p, vec, grid, s);
+    if (p.dy_dt == MILO_F16) return run_dz_vec<MILO_F16, ZT>(p, vec, grid, s);
+    return run_dz_vec<MILO_BF16, ZT>(p, vec, grid, s);
+}
+
+// db[n] = the row blocks' sums: eight lanes of a column take every eighth block
+// in order, and meet in lane order.
 __global__ void __launch_bounds__(256) dense_db_kernel(const float* __restrict__ part, int blocks, int N, int bf16,
                                                        uint16_t* __restrict__ db, int32_t* dev_status) {
+    __shared__ float red[8][32];
     grid_dep_launch();
     grid_dep_wait();
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
-    int32_t st = 0;
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int n = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int b = 0; b < blocks; ++b) s += part[static_cast<size_t>(b) * N + n];
+    if (n < N)
+#pragma unroll 8
+        for (int b = rl; b < blocks; b += 8) s += part[static_cast<size_t>(b) * N + n];
+    red[rl][lane] = s;
+    __syncthreads();
+    if (rl > 0 || n >= N) return;
+    int32_t st = 0;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += red[q][lane];
     db[n] = round16(s, bf16, st);
     flag(dev_status, st);
 }
@@ -155,17 +197,21 @@ static bool out_ok(milo_dtype d) { return d == MILO_F16 || d == MILO_BF16 || d =
 static uintptr_t elem(milo_dtype d) { return d == MILO_F32 ? 4 : 2; }
 
 // Scratch of the backward pass: dz [M, ldz] in the product's type (rows padded
-// to 16 bytes, as the products' tiles are copied) and the column sums of each
+// to 128 bytes, what one row of a TMA box brings) and the column sums of each
 // row block.
 struct DenseWs {
     size_t dz, part, total;
-    int ldz, blocks;
+    int ldz, rows, blocks;
 };
 
 static DenseWs dense_ws(int M, int N) {
     DenseWs w;
-    w.ldz = static_cast<int>(round_up(N, 8));
-    w.blocks = (M + kDzRows - 1) / kDzRows;
+    w.ldz = static_cast<int>(round_up(N, 64));
+    // rows of a block: 64, fewer while the blocks do not fill the SMs four deep
+    w.rows = 64;
+    const long long col_blocks = (N + kDzCols - 1) / kDzCols;
+    while (w.rows > 8 && (M + w.rows - 1) / w.rows * col_blocks < 4 * 148) w.rows /= 2;
+    w.blocks = (M + w.rows - 1) / w.rows;
     w.dz = 0;
     w.part = round_up(static_cast<size_t>(M) * w.ldz * 2, 256);
     w.total = w.part + round_up(static_cast<size_t>(w.blocks) * N * 4, 256);
@@ -233,15 +279,16 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
     const bool direct = act == MILO_ACT_NONE && dy_dt == dt && N % 8 == 0 && aligned(dy, 16);
     const bool want_dz = !direct && (dx || dW);
     if (want_dz || db) {
-        DzParams p = {dy, act == MILO_ACT_NONE ? nullptr : z, want_dz ? base + w.dz : nullptr,
-                      db ? reinterpret_cast<float*>(base + w.part) : nullptr, dev_status, M, N, w.ldz,
-                      static_cast<int>(dy_dt), dt == MILO_BF16, act,
-                      N % 8 == 0 && aligned(dy, 16) && (act == MILO_ACT_NONE || aligned(z, 16)), (w.ldz + kDzCols - 1) / kDzCols};
-        const dim3 grid(static_cast<unsigned>(w.blocks) * static_cast<unsigned>(p.col_blocks));
-        if ((s = check_cuda(launch_pdl(dense_dz_kernel, grid, dim3(kDzThreads), 0, st, p), "dz")) != MILO_OK) return s;
+        const DzParams p = {dy, act == MILO_ACT_NONE ? nullptr : z, want_dz ? base + w.dz : nullptr,
+                            db ? reinterpret_cast<float*>(base + w.part) : nullptr, dev_status, M, N, w.ldz,
+                            static_cast<int>(dy_dt), dt == MILO_BF16, act, w.rows, (w.ldz + kDzCols - 1) / kDzCols};
+        const bool vec = N % 8 == 0 && aligned(dy, 16) && (act == MILO_ACT_NONE || aligned(z, 16));
+        const int grid = w.blocks * p.col_blocks;
+        s = check_cuda(dt == MILO_BF16 ? run_dz<MILO_BF16>(p, vec, grid, st) : run_dz<MILO_F16>(p, vec, grid, st), "dz");
+        if (s != MILO_OK) return s;
     }
     if (db) {
-        s = check_cuda(launch_pdl(dense_db_kernel, dim3((N + 255) / 256), dim3(256), 0, st,
+        s = check_cuda(launch_pdl(dense_db_kernel, dim3((N + 31) / 32), dim3(256), 0, st,
                                   reinterpret_cast<const float*>(base + w.part), w.blocks, N, dt == MILO_BF16 ? 1 : 0,
                                   static_cast<uint16_t*>(db), dev_status),
                        "db");
