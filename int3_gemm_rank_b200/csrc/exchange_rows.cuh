@@ -101,9 +101,17 @@ __device__ __forceinline__ void write_cols(T* row, int v0, int lane, int nc, con
     if constexpr (AL) {
         if (v0 + 8 * lane < nc) store8<T>(row + v0 + 8 * lane, v, st);
     } else {
+        T e[8];
+        to_elems<T>(v, e, st);
+        T* d = row + v0 + lane;
+        if (v0 + 256 <= nc) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (v0 + lane + 32 * q < nc) row[v0 + lane + 32 * q] = from_f32<T>(v[q], st);
+            for (int q = 0; q < 8; ++q) d[32 * q] = e[q];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (v0 + lane + 32 * q < nc) d[32 * q] = e[q];
+        }
     }
 }
 

@@ -68,9 +68,40 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight values to a 16-byte aligned address.  FP16_RANGE: a half whose exponent
-// field is all ones (adding one there carries into the sign's place) is looked
-// at again, since an infinity may have been one before.
+// FP16_RANGE for eight values and their packed halves: one whose exponent field is
+// all ones (adding one there carries into the sign's place) is looked at again,
+// since an infinity may have been one before.
+__device__ __forceinline__ void half_overflow(const float (&v)[8], const uint32_t (&w)[4], int32_t& st) {
+    uint32_t e = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e |= (w[q] & 0x7C007C00u) + 0x04000400u;
+    if (e & 0x80008000u) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (fabsf(v[q]) >= 65520.0f && !isinf(v[q])) st |= MILO_DEV_FP16_RANGE;
+    }
+}
+
+// Eight values rounded to T.
+template <typename T>
+__device__ __forceinline__ void to_elems(const float (&v)[8], T (&e)[8], int32_t& st) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) e[q] = v[q];
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = pack2<T>(v[2 * q], v[2 * q + 1]);
+        if constexpr (std::is_same<T, __half>::value) half_overflow(v, w, st);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint16_t h = static_cast<uint16_t>(q & 1 ? w[q / 2] >> 16 : w[q / 2] & 0xFFFFu);
+            e[q] = *reinterpret_cast<const T*>(&h);
+        }
+    }
+}
+
+// Eight values to a 16-byte aligned address.
 template <typename T>
 __device__ __forceinline__ void store8(void* dst, const float (&v)[8], int32_t& st) {
     if constexpr (sizeof(T) == 4) {
@@ -81,16 +112,7 @@ __device__ __forceinline__ void store8(void* dst, const float (&v)[8], int32_t& 
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) w[q] = pack2<T>(v[2 * q], v[2 * q + 1]);
-        if constexpr (std::is_same<T, __half>::value) {
-            uint32_t e = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) e |= (w[q] & 0x7C007C00u) + 0x04000400u;
-            if (e & 0x80008000u) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (fabsf(v[q]) >= 65520.0f && !isinf(v[q])) st |= MILO_DEV_FP16_RANGE;
-            }
-        }
+        if constexpr (std::is_same<T, __half>::value) half_overflow(v, w, st);
         *static_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
