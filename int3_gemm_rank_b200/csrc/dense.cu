@@ -31,6 +31,7 @@ struct DzParams {
     const void* z;              // [M, N] or NULL
     void* dz;                   // [M, ldz] in the product's type, columns N..ldz-1 zero; NULL: not written
     float* part;                // [row blocks][N] column sums, or NULL
+    void* db;                   // with one row block: the sums themselves, in the product's type
     int32_t* dev_status;
     int M, N, ldz, dy_dt, bf16, act;
     int rows, col_blocks;       // rows of a block; blocks of columns
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(kDzThreads) dense_dz_kernel(const DzParams p) 
             float z[8];
             dz_load<ZT, VEC>(p.z, m, p.N, n0, lane, z);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] *= act_slope<ACT>(z[q]);
+            for (int q = 0; q < 8; ++q)
+                v[q] = __fmul_rn(v[q], act_slope<ACT>(z[q]));    // no FMA into the sum: db alone has the same bits
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum[q] += v[q];
@@ -118,7 +120,10 @@ __global__ void __launch_bounds__(kDzThreads) dense_dz_kernel(const DzParams p) 
         float s = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) s += red[q][threadIdx.x];
-        if (n < p.N) p.part[static_cast<size_t>(rb) * p.N + n] = s;
+        if (n < p.N) {
+            if (p.db) elem_store<ZT>(p.db, n, s, st);
+            else p.part[static_cast<size_t>(rb) * p.N + n] = s;
+        }
     }
     flag(p.dev_status, st);
 }
@@ -202,10 +207,11 @@ struct DenseWs {
 static DenseWs dense_ws(int M, int N) {
     DenseWs w;
     w.ldz = static_cast<int>(round_up(N, 64));
-    // rows of a block: 64, fewer while the blocks do not fill the SMs four deep
+    // rows of a block: 64, fewer while the blocks do not fill the SMs four deep --
+    // but up to 64 rows in one, whose column sums then need no second kernel
     w.rows = 64;
     const long long col_blocks = (N + kDzCols - 1) / kDzCols;
-    while (w.rows > 8 && (M + w.rows - 1) / w.rows * col_blocks < 4 * 148) w.rows /= 2;
+    while (M > 64 && w.rows > 8 && (M + w.rows - 1) / w.rows * col_blocks < 4 * 148) w.rows /= 2;
     w.blocks = (M + w.rows - 1) / w.rows;
     w.dz = 0;
     w.part = round_up(static_cast<size_t>(M) * w.ldz * 2, 256);
@@ -275,14 +281,15 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
     const bool want_dz = !direct && (dx || dW);
     if (want_dz || db) {
         const DzParams p = {dy, act == MILO_ACT_NONE ? nullptr : z, want_dz ? base + w.dz : nullptr,
-                            db ? reinterpret_cast<float*>(base + w.part) : nullptr, dev_status, M, N, w.ldz,
+                            db ? reinterpret_cast<float*>(base + w.part) : nullptr, w.blocks == 1 ? db : nullptr,
+                            dev_status, M, N, w.ldz,
                             static_cast<int>(dy_dt), dt == MILO_BF16, act, w.rows, (w.ldz + kDzCols - 1) / kDzCols};
         const bool vec = N % 8 == 0 && aligned(dy, 16) && (act == MILO_ACT_NONE || aligned(z, 16));
         const int grid = w.blocks * p.col_blocks;
         s = check_cuda(dt == MILO_BF16 ? run_dz<MILO_BF16>(p, vec, grid, st) : run_dz<MILO_F16>(p, vec, grid, st), "dz");
         if (s != MILO_OK) return s;
     }
-    if (db) {
+    if (db && w.blocks > 1) {
         s = check_cuda(launch_pdl(dense_db_kernel, dim3((N + 31) / 32), dim3(256), 0, st,
                                   reinterpret_cast<const float*>(base + w.part), w.blocks, N, dt == MILO_BF16 ? 1 : 0,
                                   static_cast<uint16_t*>(db), dev_status),
@@ -291,15 +298,9 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
     }
     const void* dz = direct ? dy : base + w.dz;
     const long long ldz = direct ? N : w.ldz;
-    if (dx) {
-        const DenseGemm g = {dz, W, ldz, K, 0, 1, M, K, N, dt == MILO_BF16, nullptr, nullptr, MILO_ACT_NONE, dx, dt,
-                             nullptr, dev_status};
-        if ((s = launch_dense_gemm(g, "dx", st)) != MILO_OK) return s;
-    }
-    if (dW) {
-        const DenseGemm g = {dz, x, ldz, K, 1, 1, N, K, M, dt == MILO_BF16, nullptr, nullptr, MILO_ACT_NONE, dW, dt,
-                             nullptr, dev_status};
-        if ((s = launch_dense_gemm(g, "dW", st)) != MILO_OK) return s;
-    }
-    return MILO_OK;
+    const DenseGemm gx = {dz, W, ldz, K, 0, 1, M, K, N, dt == MILO_BF16, nullptr, nullptr, MILO_ACT_NONE, dx, dt,
+                          nullptr, dev_status};
+    const DenseGemm gw = {dz, x, ldz, K, 1, 1, N, K, M, dt == MILO_BF16, nullptr, nullptr, MILO_ACT_NONE, dW, dt,
+                          nullptr, dev_status};
+    return launch_dense_pair(gx, gw, "dx and dW", st);
 }

@@ -13,6 +13,8 @@
 //     they are stored by the forward product and by both gradients.
 //   - Many tiles: a persistent grid, two accumulators in TMEM, so that the
 //     epilogue of one tile runs under the products of the next.
+//   - Two products may share a launch (a layer's dx and dW): their tiles follow
+//     one another on the same grid, so neither's last wave leaves SMs idle.
 //   - Few tiles: c is split over the CTAs of a cluster.  The tile's blocks of
 //     32 rows by 32 (SWAP: 16) columns are dealt out to the CTAs; each sends its
 //     partial blocks to their owners' shared memory, and after a cluster
@@ -55,19 +57,28 @@ constexpr int kDtBias = 128;                 // fp32 bias columns, per epilogue 
 // banks.
 constexpr int dense_pitch(int esize) { return 32 * esize + 16; }
 
-struct DenseTc {
+// One product of a launch.
+struct DenseProb {
     CUtensorMap a_map, b_map;
     int P, Q, C;
-    int a_mn, b_mn, bf16;
-    int bn, stages, split, kblocks;          // columns of a tile; c slices of 64
+    int a_mn, b_mn;
+    int kblocks;                             // slices of 64 c
     int tiles_p, tiles_q, tiles;
-    uint32_t idesc, tmem_cols;
+    uint32_t idesc;
+    int vec;                                 // 16-byte output rows
+    void* y;                                 // [P, Q] (SWAP: [Q, P])
+};
+
+struct DenseTc {
+    DenseProb prob[2];                       // one product, or two that share the grid (a layer's dx and dW)
+    int tiles;                               // of both
+    int bf16, bn, stages, split;             // columns of a tile; CTAs that share a tile's c
+    uint32_t tmem_cols;
     int bufs;                                // accumulators in TMEM (2: persistent)
     int stage_bytes, staging, off_staging, off_bias, off_bar;
-    int vec;                                 // 16-byte output rows
-    // epilogue (y, residual and z are [M, N]; SWAP: p is the feature)
+    // epilogue (residual and z as y; SWAP: p is the feature)
     const void *bias, *residual;
-    void *y, *z;
+    void* z;
     int act, y_dt;
     int32_t* dev_status;
 };
@@ -105,12 +116,21 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
 // Item order: bands of kDtBand row tiles, columns inside a band, the band's
 // row tiles fastest, so that the CTAs at work share operand tiles in L2.
 constexpr int kDtBand = 16;
-__device__ __forceinline__ void dense_tile(const DenseTc& p, int item, int& tp, int& tq) {
-    const int per = kDtBand * p.tiles_q;
+struct DenseItem {
+    int i;                                   // product
+    int tp, tq;
+};
+__device__ __forceinline__ DenseItem dense_tile(const DenseTc& p, int item) {
+    DenseItem r;
+    r.i = item >= p.prob[0].tiles;
+    if (r.i) item -= p.prob[0].tiles;
+    const DenseProb& d = p.prob[r.i];
+    const int per = kDtBand * d.tiles_q;
     const int band = item / per, in = item - band * per;
-    const int h = min(kDtBand, p.tiles_p - band * kDtBand);
-    tq = in / h;
-    tp = band * kDtBand + in - tq * h;
+    const int h = min(kDtBand, d.tiles_p - band * kDtBand);
+    r.tq = in / h;
+    r.tp = band * kDtBand + in - r.tq * h;
+    return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -119,21 +139,21 @@ __device__ __forceinline__ void dense_tile(const DenseTc& p, int item, int& tp, 
 // ---------------------------------------------------------------------------
 
 // The warp's 32 x 32 block between staging rows and global rows p0.., columns
-// q0..; 16-byte pieces when p.vec.
+// q0..; 16-byte pieces when d.vec.
 template <int DT, bool LOAD>
-__device__ __forceinline__ void dense_block(const DenseTc& p, void* g, uint8_t* stg, int p0, int q0, int lane) {
+__device__ __forceinline__ void dense_block(const DenseTc& p, const DenseProb& d, void* g, uint8_t* stg, int p0, int q0, int lane) {
     constexpr int E = DT == MILO_F32 ? 4 : 2, kPitch = dense_pitch(E);
     constexpr int kPieces = 32 * E / 16;              // 16-byte pieces of a row
     constexpr int kRows = 32 / kPieces;               // rows of one pass
-    if (p.vec) {
+    if (d.vec) {
         const int piece = lane % kPieces, r0 = lane / kPieces;
-        const bool in = q0 + piece * (16 / E) < p.Q;  // Q is a multiple of a piece here
-        uint8_t* gp = static_cast<uint8_t*>(g) + (static_cast<size_t>(p0 + r0) * p.Q + q0) * E + piece * 16;
+        const bool in = q0 + piece * (16 / E) < d.Q;  // Q is a multiple of a piece here
+        uint8_t* gp = static_cast<uint8_t*>(g) + (static_cast<size_t>(p0 + r0) * d.Q + q0) * E + piece * 16;
         uint4 t[32 / kRows];
 #pragma unroll
         for (int i = 0; i < 32 / kRows; ++i) {
             if constexpr (LOAD) {
-                if (in && p0 + r0 + i * kRows < p.P) t[i] = *reinterpret_cast<const uint4*>(gp + static_cast<size_t>(i) * kRows * p.Q * E);
+                if (in && p0 + r0 + i * kRows < d.P) t[i] = *reinterpret_cast<const uint4*>(gp + static_cast<size_t>(i) * kRows * d.Q * E);
             } else {
                 t[i] = *reinterpret_cast<const uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16);
             }
@@ -143,19 +163,19 @@ __device__ __forceinline__ void dense_block(const DenseTc& p, void* g, uint8_t* 
             if constexpr (LOAD) {
                 *reinterpret_cast<uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16) = t[i];
             } else {
-                if (in && p0 + r0 + i * kRows < p.P) *reinterpret_cast<uint4*>(gp + static_cast<size_t>(i) * kRows * p.Q * E) = t[i];
+                if (in && p0 + r0 + i * kRows < d.P) *reinterpret_cast<uint4*>(gp + static_cast<size_t>(i) * kRows * d.Q * E) = t[i];
             }
         }
     } else {
         using T = typename std::conditional<E == 4, uint32_t, uint16_t>::type;
-        if (q0 + lane < p.Q) {
-            T* gp = static_cast<T*>(g) + static_cast<size_t>(p0) * p.Q + q0 + lane;
+        if (q0 + lane < d.Q) {
+            T* gp = static_cast<T*>(g) + static_cast<size_t>(p0) * d.Q + q0 + lane;
             T* sp = reinterpret_cast<T*>(stg) + lane;
-            const int n = min(32, p.P - p0);
+            const int n = min(32, d.P - p0);
 #pragma unroll 8
             for (int r = 0; r < n; ++r) {
-                if constexpr (LOAD) sp[r * (kPitch / E)] = gp[static_cast<size_t>(r) * p.Q];
-                else gp[static_cast<size_t>(r) * p.Q] = sp[r * (kPitch / E)];
+                if constexpr (LOAD) sp[r * (kPitch / E)] = gp[static_cast<size_t>(r) * d.Q];
+                else gp[static_cast<size_t>(r) * d.Q] = sp[r * (kPitch / E)];
             }
         }
     }
@@ -163,7 +183,7 @@ __device__ __forceinline__ void dense_block(const DenseTc& p, void* g, uint8_t* 
 
 // The lane's 32 values to its staging row, and the block to global memory.
 template <int DT>
-__device__ __forceinline__ void dense_put(const DenseTc& p, void* g, const float (&v)[32], uint8_t* stg, int p0, int q0,
+__device__ __forceinline__ void dense_put(const DenseTc& p, const DenseProb& d, void* g, const float (&v)[32], uint8_t* stg, int p0, int q0,
                                           int lane, int32_t& st) {
     uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
     if constexpr (DT == MILO_F32) {
@@ -180,14 +200,14 @@ __device__ __forceinline__ void dense_put(const DenseTc& p, void* g, const float
             reinterpret_cast<uint4*>(row)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
     __syncwarp();
-    dense_block<DT, false>(p, g, stg, p0, q0, lane);
+    dense_block<DT, false>(p, d, g, stg, p0, q0, lane);
     __syncwarp();
 }
 
 // v += the block of the residual.
 template <int DT>
-__device__ __forceinline__ void dense_add(const DenseTc& p, float (&v)[32], uint8_t* stg, int p0, int q0, int lane) {
-    dense_block<DT, true>(p, const_cast<void*>(p.residual), stg, p0, q0, lane);
+__device__ __forceinline__ void dense_add(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg, int p0, int q0, int lane) {
+    dense_block<DT, true>(p, d, const_cast<void*>(p.residual), stg, p0, q0, lane);
     __syncwarp();
     const uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
     if constexpr (DT == MILO_F32) {
@@ -211,7 +231,7 @@ __device__ __forceinline__ void dense_add(const DenseTc& p, float (&v)[32], uint
     __syncwarp();
 }
 
-__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[32], uint8_t* stg, const float* bias,
+__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg, const float* bias,
                                                   int p0, int q0, int lane, int32_t& st) {
     if (p.bias) {
 #pragma unroll
@@ -224,36 +244,36 @@ __device__ __forceinline__ void dense_store_chunk(const DenseTc& p, float (&v)[3
         }
     }
     if (p.z) {
-        if (p.bf16) dense_put<MILO_BF16>(p, p.z, v, stg, p0, q0, lane, st);
-        else dense_put<MILO_F16>(p, p.z, v, stg, p0, q0, lane, st);
+        if (p.bf16) dense_put<MILO_BF16>(p, d, p.z, v, stg, p0, q0, lane, st);
+        else dense_put<MILO_F16>(p, d, p.z, v, stg, p0, q0, lane, st);
     }
     act_tile(p.act, v);
     with_dtype(p.y_dt, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (p.residual) dense_add<DT>(p, v, stg, p0, q0, lane);
-        dense_put<DT>(p, p.y, v, stg, p0, q0, lane, st);
+        if (p.residual) dense_add<DT>(p, d, v, stg, p0, q0, lane);
+        dense_put<DT>(p, d, d.y, v, stg, p0, q0, lane, st);
     });
 }
 
 // Swapped form: the lane's row is feature p0 + lane, its N values tokens q0..:
 // y[q, p], consecutive lanes at consecutive addresses.
 template <int N>
-__device__ __forceinline__ void dense_store_swapped(const DenseTc& p, float (&v)[N], int p0, int q0, int lane,
+__device__ __forceinline__ void dense_store_swapped(const DenseTc& p, const DenseProb& d, float (&v)[N], int p0, int q0, int lane,
                                                     int32_t& st) {
     const int f = p0 + lane;
-    if (f >= p.P) return;
+    if (f >= d.P) return;
     if (p.bias) {
         const float b = load16(p.bias, f, p.bf16);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += b;
     }
-    const int n = min(N, p.Q - q0);
-    const size_t o = static_cast<size_t>(q0) * p.P + f;
+    const int n = min(N, d.Q - q0);
+    const size_t o = static_cast<size_t>(q0) * d.P + f;
     if (p.z)
         with_dtype(p.bf16 ? MILO_BF16 : MILO_F16, [&](auto dt) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (i < n) elem_store<decltype(dt)::value>(p.z, o + static_cast<size_t>(i) * p.P, v[i], st);
+                if (i < n) elem_store<decltype(dt)::value>(p.z, o + static_cast<size_t>(i) * d.P, v[i], st);
         });
     act_tile(p.act, v);
     with_dtype(p.y_dt, [&](auto dt) {
@@ -261,13 +281,13 @@ __device__ __forceinline__ void dense_store_swapped(const DenseTc& p, float (&v)
         if (p.residual) {
             float r[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) r[i] = i < n ? elem_load<DT>(p.residual, o + static_cast<size_t>(i) * p.P) : 0.0f;
+            for (int i = 0; i < N; ++i) r[i] = i < n ? elem_load<DT>(p.residual, o + static_cast<size_t>(i) * d.P) : 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] += r[i];
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < n) elem_store<DT>(p.y, o + static_cast<size_t>(i) * p.P, v[i], st);
+            if (i < n) elem_store<DT>(d.y, o + static_cast<size_t>(i) * d.P, v[i], st);
     });
 }
 
@@ -288,8 +308,10 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     grid_dep_launch();
     if (warp == 0) {
         if (elect_one()) {
-            prefetch_map(&p.a_map);
-            prefetch_map(&p.b_map);
+            for (int i = 0; i < (p.tiles > p.prob[0].tiles ? 2 : 1); ++i) {
+                prefetch_map(&p.prob[i].a_map);
+                prefetch_map(&p.prob[i].b_map);
+            }
             for (int s = 0; s < p.stages; ++s) {
                 mbar_init(&full[s], 1);
                 mbar_init(&empty[s], 1);
@@ -318,9 +340,10 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         tbase = *tmem_slot;
     }
 
-    // this CTA's share of c (all of it without a split)
-    const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * rank / p.split);
-    const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (rank + 1) / p.split);
+    // this CTA's share of a product's c (all of it without a split)
+    const auto slice = [&](const DenseProb& d, uint32_t r) {
+        return static_cast<int>(static_cast<long long>(d.kblocks) * r / p.split);
+    };
     const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
     int32_t st_bits = 0;
     // epilogue warps: lane quarter, which half of the column blocks, own buffers
@@ -336,10 +359,11 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         bool fail = false;
         const uint32_t tx = kDtAtom + p.bn * 128;
         for (int it = first; it < p.tiles && !fail; it += step) {
-            int tp, tq;
-            dense_tile(p, it, tp, tq);
-            const int p0 = tp * kDtRows, q0 = tq * p.bn;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            const DenseItem t = dense_tile(p, it);
+            const DenseProb& d = p.prob[t.i];
+            const int p0 = t.tp * kDtRows, q0 = t.tq * p.bn;
+            const int kb1 = slice(d, rank + 1);
+            for (int kb = slice(d, rank); kb < kb1; ++kb) {
                 if (!warp_wait(&empty[stage], phase ^ 1)) {
                     fail = true;
                     break;
@@ -351,17 +375,17 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 fph = (fph & ~(1u << stage)) | (phase << stage);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(fb, tx);
-                    if (p.a_mn) {
-                        tma_load_2d(sa, &p.a_map, fb, p0, kb * kDtK);
-                        tma_load_2d(sa + kDtBox, &p.a_map, fb, p0 + 64, kb * kDtK);
+                    if (d.a_mn) {
+                        tma_load_2d(sa, &d.a_map, fb, p0, kb * kDtK);
+                        tma_load_2d(sa + kDtBox, &d.a_map, fb, p0 + 64, kb * kDtK);
                     } else {
-                        tma_load_2d(sa, &p.a_map, fb, kb * kDtK, p0);
+                        tma_load_2d(sa, &d.a_map, fb, kb * kDtK, p0);
                     }
-                    if (p.b_mn) {
+                    if (d.b_mn) {
                         for (int j = 0; j < p.bn / 64; ++j)
-                            tma_load_2d(sb + j * kDtBox, &p.b_map, fb, q0 + 64 * j, kb * kDtK);
+                            tma_load_2d(sb + j * kDtBox, &d.b_map, fb, q0 + 64 * j, kb * kDtK);
                     } else {
-                        tma_load_2d(sb, &p.b_map, fb, kb * kDtK, q0);
+                        tma_load_2d(sb, &d.b_map, fb, kb * kDtK, q0);
                     }
                 }
                 __syncwarp();
@@ -377,14 +401,17 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         int stage = 0, buf = 0;
         uint32_t phase = 0, bph = 0;
         bool fail = false;
-        const uint64_t astep = p.a_mn ? 128u : 2u, bstep = p.b_mn ? 128u : 2u;   // 16 c further, in 16-byte units
         for (int it = first; it < p.tiles && !fail; it += step) {
             if (!warp_wait(&aempty[buf], bph ^ 1)) {
                 fail = true;
                 break;
             }
             tc_fence_after();
-            const uint32_t d = tbase + static_cast<uint32_t>(buf * p.bn);
+            const DenseProb& d = p.prob[dense_tile(p, it).i];
+            const int a_mn = d.a_mn, b_mn = d.b_mn, kb0 = slice(d, rank), kb1 = slice(d, rank + 1);
+            const uint64_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;   // 16 c further, in 16-byte units
+            const uint32_t idesc = d.idesc;
+            const uint32_t acc = tbase + static_cast<uint32_t>(buf * p.bn);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!warp_wait(&full[stage], phase)) {
                     fail = true;
@@ -392,11 +419,11 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 }
                 tc_fence_after();
                 const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + kDtAtom;
-                const uint64_t da = p.a_mn ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
-                const uint64_t db = p.b_mn ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
+                const uint64_t da = a_mn ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
+                const uint64_t db = b_mn ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
 #pragma unroll
                 for (int q = 0; q < kDtK / 16; ++q)
-                    tc_mma_ss(d, da + q * astep, db + q * bstep, p.idesc, kb > kb0 || q > 0 ? 1u : 0u);
+                    tc_mma_ss(acc, da + q * astep, db + q * bstep, idesc, kb > kb0 || q > 0 ? 1u : 0u);
                 tc_commit(&empty[stage]);
                 if (++stage == p.stages) { stage = 0; phase ^= 1; }
             }
@@ -412,15 +439,15 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         int buf = 0;
         uint32_t bph = 0;
         for (int it = first; it < p.tiles; it += step) {
-            int tp, tq;
-            dense_tile(p, it, tp, tq);
-            const int p0 = tp * kDtRows + 32 * quarter, q0 = tq * p.bn;
+            const DenseItem t = dense_tile(p, it);
+            const DenseProb& d = p.prob[t.i];
+            const int p0 = t.tp * kDtRows + 32 * quarter, q0 = t.tq * p.bn;
             if constexpr (!SWAP) {
                 if (p.bias) {
                     // the columns of this warp's blocks, block after block
                     for (int i = lane; i < p.bn / 2; i += 32) {
                         const int q = q0 + (i / 32 * 2 + half) * 32 + lane;
-                        sbias[i] = q < p.Q ? load16(p.bias, q, p.bf16) : 0.0f;
+                        sbias[i] = q < d.Q ? load16(p.bias, q, p.bf16) : 0.0f;
                     }
                     __syncwarp();
                 }
@@ -432,15 +459,15 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             tc_fence_after();
             const uint32_t acc = lane_base + static_cast<uint32_t>(buf * p.bn);
             for (int c = W * half; c < p.bn; c += 2 * W) {
-                uint32_t d[W];
-                tc_ld(acc + c, d);
+                uint32_t r[W];
+                tc_ld(acc + c, r);
                 tc_wait_ld();
                 float v[W];
 #pragma unroll
-                for (int i = 0; i < W; ++i) v[i] = __uint_as_float(d[i]);
-                if (p0 >= p.P || q0 + c >= p.Q) continue;
-                if constexpr (SWAP) dense_store_swapped(p, v, p0, q0 + c, lane, st_bits);
-                else dense_store_chunk(p, v, stg, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
+                for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
+                if (p0 >= d.P || q0 + c >= d.Q) continue;
+                if constexpr (SWAP) dense_store_swapped(p, d, v, p0, q0 + c, lane, st_bits);
+                else dense_store_chunk(p, d, v, stg, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
             }
             tc_fence_before();
             __syncwarp();
@@ -452,6 +479,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         // this CTA's partial blocks to their owners: block u (rows 32 (u % 4)..,
         // columns W (u / 4)..) to CTA u % split, there at [u / split][rank], four
         // columns of a lane's row together
+        const DenseProb& d = p.prob[dense_tile(p, first).i];
+        const bool none = slice(d, rank) == slice(d, rank + 1);      // a short c leaves some CTAs nothing
         if (!warp_wait(&afull[0], 0)) st_bits |= MILO_DEV_TIMEOUT;
         tc_fence_after();
         __syncwarp();
@@ -460,14 +489,18 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         for (int c = half; c < p.bn / W; c += 2) {
             const int u = 4 * c + quarter;
             const uint32_t dst = smem_u32(smem) + (u / p.split * p.split + rank) * (W * 128) + lane * 16;
-            uint32_t d[W];
-            tc_ld(lane_base + W * c, d);
+            uint32_t r[W];
+            tc_ld(lane_base + W * c, r);
             tc_wait_ld();
+            if (none) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) r[i] = 0u;
+            }
 #pragma unroll
             for (int i = 0; i < W / 4; ++i)
                 st_peer4(dst + i * 512, u % p.split,
-                         make_float4(__uint_as_float(d[4 * i]), __uint_as_float(d[4 * i + 1]), __uint_as_float(d[4 * i + 2]),
-                                     __uint_as_float(d[4 * i + 3])));
+                         make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                                     __uint_as_float(r[4 * i + 3])));
         }
         tc_fence_before();
     }
@@ -481,12 +514,12 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         cluster_arrive();
         cluster_wait();
         if (warp >= 2) {
-            int tp, tq;
-            dense_tile(p, first, tp, tq);
+            const DenseItem t = dense_tile(p, first);
+            const DenseProb& d = p.prob[t.i];
             for (int i = ew; i * p.split + static_cast<int>(rank) < 4 * (p.bn / W); i += kDtEpiWarps) {
                 const int u = i * p.split + static_cast<int>(rank);
-                const int p0 = tp * kDtRows + 32 * (u & 3), q0 = tq * p.bn + W * (u >> 2);
-                if (p0 >= p.P || q0 >= p.Q) continue;
+                const int p0 = t.tp * kDtRows + 32 * (u & 3), q0 = t.tq * p.bn + W * (u >> 2);
+                if (p0 >= d.P || q0 >= d.Q) continue;
                 const float4* src = reinterpret_cast<const float4*>(smem + i * p.split * (W * 128)) + lane;
                 float v[W];
 #pragma unroll
@@ -494,20 +527,20 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 for (int s = 0; s < p.split; ++s)
 #pragma unroll
                     for (int j = 0; j < W / 4; ++j) {
-                        const float4 t = src[(s * (W / 4) + j) * 32];
-                        v[4 * j] += t.x;
-                        v[4 * j + 1] += t.y;
-                        v[4 * j + 2] += t.z;
-                        v[4 * j + 3] += t.w;
+                        const float4 f = src[(s * (W / 4) + j) * 32];
+                        v[4 * j] += f.x;
+                        v[4 * j + 1] += f.y;
+                        v[4 * j + 2] += f.z;
+                        v[4 * j + 3] += f.w;
                     }
                 if constexpr (SWAP) {
-                    dense_store_swapped(p, v, p0, q0, lane, st_bits);
+                    dense_store_swapped(p, d, v, p0, q0, lane, st_bits);
                 } else {
                     if (p.bias) {
-                        sbias[lane] = q0 + lane < p.Q ? load16(p.bias, q0 + lane, p.bf16) : 0.0f;
+                        sbias[lane] = q0 + lane < d.Q ? load16(p.bias, q0 + lane, p.bf16) : 0.0f;
                         __syncwarp();
                     }
-                    dense_store_chunk(p, v, stg, sbias, p0, q0, lane, st_bits);
+                    dense_store_chunk(p, d, v, stg, sbias, p0, q0, lane, st_bits);
                 }
             }
         }
@@ -542,7 +575,7 @@ static uint32_t dense_idesc(int bf16, int a_mn, int b_mn, int bn) {
 }
 
 template <bool SWAP>
-static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStream_t s) {
+static cudaError_t dense_configure() {
     static std::atomic<bool> configured[64];     // set once per device (a repeat is harmless)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -552,6 +585,13 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
     }
+    return cudaSuccess;
+}
+
+template <bool SWAP>
+static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStream_t s) {
+    const cudaError_t e = dense_configure<SWAP>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kDtThreads);
@@ -569,57 +609,135 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
     return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP>, p);
 }
 
+// Clusters of `split` CTAs (with a whole SM's shared memory each) that run at
+// once on the current device; asked once per device and size.
+static int max_clusters(int split) {
+    static std::atomic<int> known[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    const int at = split == 2 ? 1 : split == 4 ? 2 : 3;
+    int n = known[dev][at].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (dense_configure<false>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(split));
+    cfg.blockDim = dim3(kDtThreads);
+    cfg.dynamicSmemBytes = kDtSmemMax + 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, dense_tc_kernel<false>, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][at].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Columns of a tile and split of c, by an estimate in SM cycles of a CTA's
-// work: a slice of c takes bn * 2 cycles of the tensor core or its bytes at 90
-// bytes a cycle (what one SM was seen to draw from L2), whichever is longer; a
-// wave of tiles takes its slices and, when nothing follows to hide it, an
-// epilogue; all of it at least the operands' bytes at the measured copy rate
-// (3.4 bytes a cycle and SM each way, at 148 SMs and 1.9 GHz: 23 in all).
-static void dense_plan(DenseTc& p, bool swap, int sms) {
-    double best = -1.0;
-    const double dram = (static_cast<double>(p.P) + p.Q) * p.C * 2.0 / (23.0 * 148.0);
-    const int bn_swap = static_cast<int>(round_up(p.Q, 16));
-    for (int bn = swap ? bn_swap : 64; bn <= (swap ? bn_swap : 256); bn *= 2) {
-        if (!swap && bn > 64 && bn / 2 >= p.Q) break;            // the tile would be mostly empty
-        const double tiles = std::ceil(p.P / 128.0) * std::ceil(p.Q / static_cast<double>(bn));
-        const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 90.0);
-        for (int split = 1; split <= kDtMaxSplit && (split == 1 || p.kblocks >= 2 * split); split *= 2) {
-            const double waves = std::ceil(tiles * split / sms);
-            if (split > 1 && waves > 1.0) break;                 // clusters only where one wave holds them
+// work: a slice of c takes bn * 2 cycles of the tensor core or its bytes at 66
+// bytes a cycle (what one SM was seen to draw from L2: 0.385 us for the 48 KB
+// of a 256-column slice), whichever is longer; a wave of tiles takes its
+// slices, and the last one an epilogue; all of it at least the operands' bytes
+// at the measured copy rate (23 bytes a cycle and SM).
+static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, int* bn_out, int* split_out) {
+    double best = -1.0, dram = 0.0;
+    int qmax = 0, kmax = 0;
+    double P[2], Q[2], kblocks[2];
+    for (int i = 0; i < n; ++i) {
+        P[i] = swap ? gs[i].Q : gs[i].P;
+        Q[i] = swap ? gs[i].P : gs[i].Q;
+        kblocks[i] = (gs[i].C + kDtK - 1) / kDtK;
+        dram += (P[i] + Q[i]) * gs[i].C * 2.0 / (23.0 * 148.0);
+        qmax = std::max(qmax, static_cast<int>(Q[i]));
+        kmax = std::max(kmax, static_cast<int>(kblocks[i]));
+    }
+    const int bn_swap = static_cast<int>(round_up(qmax, 16));
+    for (int bn = swap ? bn_swap : 64; bn <= (swap ? bn_swap : 256); bn += 64) {
+        if (!swap && bn > 64 && bn - 64 >= qmax) break;          // the tile would be part empty
+        const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 66.0);
+        for (int split = 1; split <= kDtMaxSplit && (split == 1 || kmax >= 2 * split); split *= 2) {
+            double tiles = 0.0, slices = 0.0, longest = 0.0;
+            for (int i = 0; i < n; ++i) {
+                const double t = std::ceil(P[i] / 128.0) * std::ceil(Q[i] / static_cast<double>(bn));
+                const double k = std::ceil(kblocks[i] / split);
+                tiles += t;
+                slices += t * k;
+                longest = std::max(longest, k);
+            }
+            // clusters only where one wave holds them all
+            if (split > 1 && tiles > max_clusters(split)) break;
+            const double waves = split > 1 ? 1.0 : std::ceil(tiles / sms);
+            const double work = waves == 1.0 ? longest : std::max(longest, waves * slices / tiles);
             const double epilogue = 8.0 * bn * (split > 1 ? 1.0 / split : 1.0);
-            const double cost = std::max(dram, waves * std::ceil(p.kblocks / static_cast<double>(split)) * slice) + epilogue +
+            const double cost = std::max(dram, (work + 0.5 * waves) * slice) + epilogue +
                                 (split > 1 ? 1500.0 + 100.0 * split : 0.0);
             if (best < 0.0 || cost < best) {
                 best = cost;
-                p.bn = bn;
-                p.split = split;
+                *bn_out = bn;
+                *split_out = split;
             }
         }
     }
-    p.tiles_p = (p.P + kDtRows - 1) / kDtRows;
-    p.tiles_q = (p.Q + p.bn - 1) / p.bn;
+    return best;
 }
 
-milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
-    if (g.P <= kDenseFewRows && !g.a_mn && !g.b_mn) return launch_dense_few(g, what, s);
+// n products (two share a grid and an epilogue without bias, residual, z and
+// act).  One without an output only takes part in the plan, so that the other's
+// sums do not depend on it.
+static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const char* what, cudaStream_t s) {
     DenseTc p;
     memset(&p, 0, sizeof(p));
-    // few rows of A (tokens): they become the columns
-    const bool swap = g.P <= 128 && !g.a_mn;
-    p.P = swap ? g.Q : g.P;
-    p.Q = swap ? g.P : g.Q;
-    p.C = g.C;
-    p.a_mn = swap ? g.b_mn : g.a_mn;
-    p.b_mn = swap ? g.a_mn : g.b_mn;
-    const void* a = swap ? g.b : g.a;
-    const void* b = swap ? g.a : g.b;
-    const long long lda = swap ? g.ldb : g.lda, ldb = swap ? g.lda : g.ldb;
-    p.bf16 = g.bf16;
-    p.kblocks = (p.C + kDtK - 1) / kDtK;
+    const void *a[2] = {}, *b[2] = {};
+    long long lda[2] = {}, ldb[2] = {};
+    for (int i = 0; i < n; ++i) {
+        const DenseGemm& g = gs[i];
+        DenseProb& d = p.prob[i];
+        d.P = swap ? g.Q : g.P;
+        d.Q = swap ? g.P : g.Q;
+        d.C = g.C;
+        d.a_mn = swap ? g.b_mn : g.a_mn;
+        d.b_mn = swap ? g.a_mn : g.b_mn;
+        a[i] = swap ? g.b : g.a;
+        b[i] = swap ? g.a : g.b;
+        lda[i] = swap ? g.ldb : g.lda;
+        ldb[i] = swap ? g.lda : g.ldb;
+        d.kblocks = (d.C + kDtK - 1) / kDtK;
+        d.y = g.y;
+        d.vec = g.Q % 8 == 0 && aligned(g.y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
+    }
+    const DenseGemm& g = gs[0];
     const int sms = dense_sms();
-    dense_plan(p, swap, sms);
-    const long long tiles = static_cast<long long>(p.tiles_p) * p.tiles_q;
-    if (tiles > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
+    dense_plan(gs, n, swap, sms, &p.bn, &p.split);
+    int live = 0;
+    for (int i = 0; i < n; ++i)
+        if (p.prob[i].y) {
+            p.prob[live] = p.prob[i];
+            a[live] = a[i];
+            b[live] = b[i];
+            lda[live] = lda[i];
+            ldb[live] = ldb[i];
+            ++live;
+        }
+    if (live < n) memset(&p.prob[live], 0, sizeof(DenseProb));
+    n = live;
+    p.bf16 = g.bf16;
+    long long tiles = 0;
+    int kper = 0;
+    for (int i = 0; i < n; ++i) {
+        DenseProb& d = p.prob[i];
+        d.tiles_p = (d.P + kDtRows - 1) / kDtRows;
+        d.tiles_q = (d.Q + p.bn - 1) / p.bn;
+        const long long t = static_cast<long long>(d.tiles_p) * d.tiles_q;
+        if ((tiles += t) > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
+        d.tiles = static_cast<int>(t);
+        d.idesc = dense_idesc(p.bf16, d.a_mn, d.b_mn, p.bn);
+        kper = std::max(kper, (d.kblocks + p.split - 1) / p.split);
+    }
     p.tiles = static_cast<int>(tiles);
     p.bufs = p.split == 1 && p.tiles > sms ? 2 : 1;
     p.stage_bytes = kDtAtom + p.bn * 128;
@@ -629,7 +747,6 @@ milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t
     const int staging = kDtEpiWarps * p.staging, bias = swap ? 0 : kDtEpiWarps * kDtBias * 4;
     const int w = swap ? 16 : kDtChunk;
     const int part = p.split > 1 ? static_cast<int>(round_up(4 * (p.bn / w), p.split)) * w * 128 : 0;
-    const int kper = (p.kblocks + p.split - 1) / p.split;
     p.stages = std::min({kDtMaxStages, (kDtSmemMax - staging - bias - 512) / p.stage_bytes,
                          std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
     p.off_staging = std::max(p.stages * p.stage_bytes, part);
@@ -638,27 +755,48 @@ milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t
     const int smem = p.off_bar + 512 + 1024;
     p.tmem_cols = 32;
     while (p.tmem_cols < static_cast<uint32_t>(p.bufs * p.bn)) p.tmem_cols *= 2;
-    p.idesc = dense_idesc(p.bf16, p.a_mn, p.b_mn, p.bn);
     p.bias = g.bias;
     p.residual = g.residual;
-    p.y = g.y;
     p.z = g.z;
     p.act = g.act;
     p.y_dt = g.y_dt;
     p.dev_status = g.dev_status;
-    p.vec = g.Q % 8 == 0 && aligned(g.y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
 
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    milo_status st;
-    // K-major [rows, c]: box 64 c by the tile's rows; MN-major [c, rows]: box 64 rows by 64 c
-    st = p.a_mn ? make_map(&p.a_map, a, dt, p.P, p.C, lda * 2, 64, kDtK, what, CU_TENSOR_MAP_SWIZZLE_128B)
-                : make_map(&p.a_map, a, dt, p.C, p.P, lda * 2, kDtK, kDtRows, what, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (st != MILO_OK) return st;
-    st = p.b_mn ? make_map(&p.b_map, b, dt, p.Q, p.C, ldb * 2, 64, kDtK, what, CU_TENSOR_MAP_SWIZZLE_128B)
-                : make_map(&p.b_map, b, dt, p.C, p.Q, ldb * 2, kDtK, p.bn, what, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (st != MILO_OK) return st;
+    const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
+    for (int i = 0; i < n; ++i) {
+        // K-major [rows, c]: box 64 c by the tile's rows; MN-major [c, rows]: box 64 rows by 64 c
+        DenseProb& d = p.prob[i];
+        milo_status st = d.a_mn ? make_map(&d.a_map, a[i], dt, d.P, d.C, lda[i] * 2, 64, kDtK, what, swz)
+                                : make_map(&d.a_map, a[i], dt, d.C, d.P, lda[i] * 2, kDtK, kDtRows, what, swz);
+        if (st != MILO_OK) return st;
+        st = d.b_mn ? make_map(&d.b_map, b[i], dt, d.Q, d.C, ldb[i] * 2, 64, kDtK, what, swz)
+                    : make_map(&d.b_map, b[i], dt, d.C, d.Q, ldb[i] * 2, kDtK, p.bn, what, swz);
+        if (st != MILO_OK) return st;
+    }
     const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
     return check_cuda(swap ? launch_dense_tc<true>(p, grid, smem, s) : launch_dense_tc<false>(p, grid, smem, s), what);
+}
+
+milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
+    if (g.P <= kDenseFewRows && !g.a_mn && !g.b_mn) return launch_dense_few(g, what, s);
+    // few rows of A (tokens): they become the columns
+    return launch_dense(&g, 1, g.P <= 128 && !g.a_mn, what, s);
+}
+
+milo_status launch_dense_pair(const DenseGemm& g0, const DenseGemm& g1, const char* what, cudaStream_t s) {
+    // the longer sums first: the shorter ones fill the last wave
+    const DenseGemm gs[2] = {g0.C >= g1.C ? g0 : g1, g0.C >= g1.C ? g1 : g0};
+    if (!g0.y && !g1.y) return MILO_OK;
+    // one launch unless the two want different tiles or splits by more than a
+    // second launch costs (about 4000 cycles)
+    int bn, split;
+    const int sms = dense_sms();
+    const double apart = dense_plan(&g0, 1, false, sms, &bn, &split) + dense_plan(&g1, 1, false, sms, &bn, &split) + 4000.0;
+    if (dense_plan(gs, 2, false, sms, &bn, &split) <= apart) return launch_dense(gs, 2, false, what, s);
+    milo_status r = g0.y ? launch_dense(&g0, 1, false, what, s) : MILO_OK;
+    if (r == MILO_OK && g1.y) r = launch_dense(&g1, 1, false, what, s);
+    return r;
 }
 
 }  // namespace milo

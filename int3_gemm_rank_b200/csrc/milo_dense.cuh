@@ -179,6 +179,9 @@ __device__ __forceinline__ void store_any(void* p, size_t i, int dt, float v, in
 constexpr int kDenseFewRows = 16;
 
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s);       // dense_tc.cu
+// Two products without an epilogue, of the same types, in one launch; one whose y
+// is NULL is left out, and the other's bits do not depend on that.
+milo_status launch_dense_pair(const DenseGemm& g0, const DenseGemm& g1, const char* what, cudaStream_t s);
 milo_status launch_dense_few(const DenseGemm& g, const char* what, cudaStream_t s);        // dense_few.cu
 
 }  // namespace milo

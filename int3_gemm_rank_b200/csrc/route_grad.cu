@@ -31,15 +31,18 @@ struct RouteGradArgs {
 // its 32 lanes (65536 x 64, k 6: 18.7 us that way).  The k <= KM picks are few
 // and read by all L lanes (one L1 line) before anything else, each lane adding
 // those that are its own.
-template <typename TO, int L, int KM>
+template <typename TO, int L, int KM, bool VEC>
 __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradArgs p) {
     grid_dep_launch();
     grid_dep_wait();
     const long long i = static_cast<long long>(blockIdx.x) * kRgThreads + threadIdx.x;
     const bool in = i / L < p.T;                          // the last warp may be part empty
     const long long t = in ? i / L : p.T - 1;
-    const int e0 = static_cast<int>(i % L) * 8;
     const int E = p.E, k = p.k;
+    // the lane's experts: eight in a row, or every L-th where rows do not start on
+    // 16-byte boundaries
+    constexpr int step = VEC ? 1 : L;
+    const int e0 = static_cast<int>(i % L) * (VEC ? 8 : 1);
     int32_t st = 0;
     float v[8], wj[KM], dj[KM];
     int id[KM];
@@ -59,12 +62,12 @@ __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradA
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = -INFINITY;
         const uint16_t* l = p.logits + t * E + e0;
-        if (p.vec) {
+        if constexpr (VEC) {
             if (e0 < E) load8<__half>(l, v);
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (e0 + q < E) v[q] = __half2float(__ushort_as_half(l[q]));
+                if (e0 + q * step < E) v[q] = __half2float(__ushort_as_half(l[q * step]));
         }
     }
     float s = 0.0f;
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradA
         float m = -INFINITY, den = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (!isfinite(v[q]) && e0 + q < E) st |= MILO_DEV_NONFINITE;
+            if (!isfinite(v[q]) && e0 + q * step < E) st |= MILO_DEV_NONFINITE;
             m = fmaxf(m, v[q]);                           // NaN counts as -inf, as in milo_route
         }
 #pragma unroll
@@ -100,16 +103,16 @@ __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradA
             const float g = p.renorm ? wj[j] * (dj[j] - s) : wj[j] * dj[j];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (id[j] == e0 + q) v[q] += g;
+                if (id[j] == e0 + q * step) v[q] += g;
         }
     if (!in) return;
     TO* d = static_cast<TO*>(p.dl) + t * E + e0;
-    if (p.vec) {
+    if constexpr (VEC) {
         if (e0 < E) store8<TO>(d, v, st);
     } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (e0 + q < E) d[q] = from_f32<TO>(v[q], st);
+            if (e0 + q * step < E) d[q * step] = from_f32<TO>(v[q], st);
     }
     flag(p.dev_status, st);
 }
@@ -117,7 +120,9 @@ __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradA
 template <typename TO, int L>
 static cudaError_t run_route_grad_l(const RouteGradArgs& a, cudaStream_t s) {
     const long long blocks = (static_cast<long long>(a.T) * L + kRgThreads - 1) / kRgThreads;
-    return launch_pdl(a.k <= 8 ? route_grad_kernel<TO, L, 8> : route_grad_kernel<TO, L, 16>, dim3(static_cast<unsigned>(blocks)), dim3(kRgThreads), 0, s, a);
+    auto k = a.vec ? (a.k <= 8 ? route_grad_kernel<TO, L, 8, true> : route_grad_kernel<TO, L, 16, true>)
+                   : (a.k <= 8 ? route_grad_kernel<TO, L, 8, false> : route_grad_kernel<TO, L, 16, false>);
+    return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRgThreads), 0, s, a);
 }
 
 // Lanes of a token: eight experts each.
