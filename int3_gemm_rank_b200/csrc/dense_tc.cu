@@ -13,6 +13,9 @@
 //     they are stored by the forward product and by both gradients.
 //   - Many tiles: a persistent grid, two accumulators in TMEM, so that the
 //     epilogue of one tile runs under the products of the next.
+//   - Large products: pairs of CTAs (cta_group::2) share tiles of 256 x 256; each
+//     brings 128 rows of A and of B, 32 KB a slice instead of 48, since what
+//     an SM can draw from L2 (about 66 bytes a cycle) bounds the single form.
 //   - Two products may share a launch (a layer's dx and dW): their tiles follow
 //     one another on the same grid, so neither's last wave leaves SMs idle.
 //   - Few tiles: c is split over the CTAs of a cluster.  The tile's blocks of
@@ -73,6 +76,7 @@ struct DenseTc {
     DenseProb prob[2];                       // one product, or two that share the grid (a layer's dx and dW)
     int tiles;                               // of both
     int bf16, bn, stages, split;             // columns of a tile; CTAs that share a tile's c
+    int two;                                 // pairs of CTAs on tiles of 256 rows
     uint32_t tmem_cols;
     int bufs;                                // accumulators in TMEM (2: persistent)
     int stage_bytes, staging, off_staging, off_bias, off_bar;
@@ -98,6 +102,46 @@ __device__ __forceinline__ void st_peer4(uint32_t saddr, uint32_t rank, float4 v
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// Pairs of CTAs (cta_group::2): the same shared-memory address in CTA `rank` of
+// the cluster, and the forms of the TMEM, copy, MMA and commit instructions that
+// work for both.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// To this CTA's shared memory, completing on a barrier of either CTA (no multicast).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss2(uint32_t d_addr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_addr), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// One arrival on this barrier in both CTAs.
+__device__ __forceinline__ void tc_commit2(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
 // Matrix descriptor of an MN-major operand in the 128-byte swizzled layout:
@@ -291,7 +335,7 @@ __device__ __forceinline__ void dense_store_swapped(const DenseTc& p, const Dens
     });
 }
 
-template <bool SWAP>
+template <bool SWAP, bool TWO>
 __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_constant__ DenseTc p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -302,8 +346,11 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     uint64_t* done_bar = aempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = p.split > 1 ? cluster_rank() : 0u;
-    constexpr int W = SWAP ? 16 : kDtChunk;      // columns of a block of the split epilogue
+    const uint32_t cta = TWO || p.split > 1 ? cluster_rank() : 0u;
+    const uint32_t rank = TWO ? 0u : cta;        // of a split of c
+    constexpr int W = SWAP ? 16 : kDtChunk;      // columns of a block of the epilogue
+    constexpr int kTileRows2 = TWO ? 2 * kDtRows : kDtRows;
+    const int group = TWO ? 2 : p.split;         // CTAs of a tile
 
     grid_dep_launch();
     if (warp == 0) {
@@ -318,7 +365,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&afull[b], 1);
-                mbar_init(&aempty[b], kDtEpiWarps);
+                mbar_init(&aempty[b], TWO ? 2 * kDtEpiWarps : kDtEpiWarps);
             }
             mbar_init(done_bar, 1);
             fence_barrier_init();
@@ -330,7 +377,16 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     // does not wait for it.
     grid_dep_wait();
     uint32_t tbase = 0;
-    if (warp == 0) {
+    if constexpr (TWO) {
+        // both CTAs' barriers and columns exist before either's copies and products
+        if (warp == 1) tmem_alloc2(tmem_slot, p.tmem_cols);
+        tc_fence_before();
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        tc_fence_after();
+        tbase = *tmem_slot;
+    } else if (warp == 0) {
         asm volatile("bar.arrive 1, %0;" ::"n"(kDtThreads) : "memory");
     } else {
         if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
@@ -344,7 +400,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     const auto slice = [&](const DenseProb& d, uint32_t r) {
         return static_cast<int>(static_cast<long long>(d.kblocks) * r / p.split);
     };
-    const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
+    const int first = static_cast<int>(blockIdx.x) / group, step = static_cast<int>(gridDim.x) / group;
     int32_t st_bits = 0;
     // epilogue warps: lane quarter, which half of the column blocks, own buffers
     const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
@@ -357,11 +413,12 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         int stage = 0;
         uint32_t phase = 0, filled = 0, fph = 0;
         bool fail = false;
-        const uint32_t tx = kDtAtom + p.bn * 128;
+        const uint32_t tx = (TWO ? 2 : 1) * p.stage_bytes;
+        const int bq = TWO ? p.bn / 2 : p.bn;        // B rows this CTA brings
         for (int it = first; it < p.tiles && !fail; it += step) {
             const DenseItem t = dense_tile(p, it);
             const DenseProb& d = p.prob[t.i];
-            const int p0 = t.tp * kDtRows, q0 = t.tq * p.bn;
+            const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0), q0 = t.tq * p.bn + (TWO ? bq * cta : 0);
             const int kb1 = slice(d, rank + 1);
             for (int kb = slice(d, rank); kb < kb1; ++kb) {
                 if (!warp_wait(&empty[stage], phase ^ 1)) {
@@ -374,18 +431,23 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 filled |= 1u << stage;
                 fph = (fph & ~(1u << stage)) | (phase << stage);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(fb, tx);
+                    // a pair's copies complete on the first CTA's barrier
+                    const uint32_t pb = TWO ? peer_addr(fb, 0) : 0u;
+                    auto load = [&](void* dst, const CUtensorMap* map, int x, int y) {
+                        if constexpr (TWO) tma_load_2d_pair(dst, map, pb, x, y);
+                        else tma_load_2d(dst, map, fb, x, y);
+                    };
+                    if (!TWO || cta == 0) mbar_arrive_expect_tx(fb, tx);
                     if (d.a_mn) {
-                        tma_load_2d(sa, &d.a_map, fb, p0, kb * kDtK);
-                        tma_load_2d(sa + kDtBox, &d.a_map, fb, p0 + 64, kb * kDtK);
+                        load(sa, &d.a_map, p0, kb * kDtK);
+                        load(sa + kDtBox, &d.a_map, p0 + 64, kb * kDtK);
                     } else {
-                        tma_load_2d(sa, &d.a_map, fb, kb * kDtK, p0);
+                        load(sa, &d.a_map, kb * kDtK, p0);
                     }
                     if (d.b_mn) {
-                        for (int j = 0; j < p.bn / 64; ++j)
-                            tma_load_2d(sb + j * kDtBox, &d.b_map, fb, q0 + 64 * j, kb * kDtK);
+                        for (int j = 0; j < bq / 64; ++j) load(sb + j * kDtBox, &d.b_map, q0 + 64 * j, kb * kDtK);
                     } else {
-                        tma_load_2d(sb, &d.b_map, fb, kb * kDtK, q0);
+                        load(sb, &d.b_map, kb * kDtK, q0);
                     }
                 }
                 __syncwarp();
@@ -393,7 +455,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             }
         }
         // no copy may still be landing in shared memory when the CTA leaves
-        for (int s = 0; s < p.stages; ++s)
+        // (a pair's first CTA sees both CTAs' copies)
+        for (int s = 0; s < p.stages && (!TWO || cta == 0); ++s)
             if (((filled >> s) & 1u) && !warp_wait(&full[s], (fph >> s) & 1u)) fail = true;
         if (fail) st_bits |= MILO_DEV_TIMEOUT;
     } else if (warp == 1) {
@@ -401,7 +464,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         int stage = 0, buf = 0;
         uint32_t phase = 0, bph = 0;
         bool fail = false;
-        for (int it = first; it < p.tiles && !fail; it += step) {
+        for (int it = first; it < p.tiles && !fail && (!TWO || cta == 0); it += step) {
             if (!warp_wait(&aempty[buf], bph ^ 1)) {
                 fail = true;
                 break;
@@ -422,26 +485,37 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 const uint64_t da = a_mn ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
                 const uint64_t db = b_mn ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb);
 #pragma unroll
-                for (int q = 0; q < kDtK / 16; ++q)
-                    tc_mma_ss(acc, da + q * astep, db + q * bstep, idesc, kb > kb0 || q > 0 ? 1u : 0u);
-                tc_commit(&empty[stage]);
+                for (int q = 0; q < kDtK / 16; ++q) {
+                    if constexpr (TWO) tc_mma_ss2(acc, da + q * astep, db + q * bstep, idesc, kb > kb0 || q > 0 ? 1u : 0u);
+                    else tc_mma_ss(acc, da + q * astep, db + q * bstep, idesc, kb > kb0 || q > 0 ? 1u : 0u);
+                }
+                if constexpr (TWO) tc_commit2(&empty[stage]);
+                else tc_commit(&empty[stage]);
                 if (++stage == p.stages) { stage = 0; phase ^= 1; }
             }
-            tc_commit(&afull[buf]);
+            if constexpr (TWO) tc_commit2(&afull[buf]);
+            else tc_commit(&afull[buf]);
             if (++buf == p.bufs) { buf = 0; bph ^= 1; }
         }
         if (fail) st_bits |= MILO_DEV_TIMEOUT;
         // every issued MMA has completed before TMEM is released
-        tc_commit(done_bar);
-        if (!warp_wait(done_bar, 0)) st_bits |= MILO_DEV_TIMEOUT;
-    } else if (p.split == 1) {
+        if constexpr (TWO) {
+            if (cta == 0) {
+                tc_commit2(done_bar);
+                if (!warp_wait(done_bar, 0)) st_bits |= MILO_DEV_TIMEOUT;
+            }
+        } else {
+            tc_commit(done_bar);
+            if (!warp_wait(done_bar, 0)) st_bits |= MILO_DEV_TIMEOUT;
+        }
+    } else if (TWO || p.split == 1) {
         // ---------------------------------------------------------------- epilogue, whole tiles
         int buf = 0;
         uint32_t bph = 0;
         for (int it = first; it < p.tiles; it += step) {
             const DenseItem t = dense_tile(p, it);
             const DenseProb& d = p.prob[t.i];
-            const int p0 = t.tp * kDtRows + 32 * quarter, q0 = t.tq * p.bn;
+            const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0) + 32 * quarter, q0 = t.tq * p.bn;
             if constexpr (!SWAP) {
                 if (p.bias) {
                     // the columns of this warp's blocks, block after block
@@ -471,7 +545,10 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&aempty[buf]);
+            if (lane == 0) {
+                if constexpr (TWO) mbar_arrive_peer(peer_addr(&aempty[buf], 0));
+                else mbar_arrive(&aempty[buf]);
+            }
             if (++buf == p.bufs) { buf = 0; bph ^= 1; }
         }
     } else {
@@ -505,7 +582,12 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         tc_fence_before();
     }
 
-    if (p.split > 1) {
+    if constexpr (TWO) {
+        // neither CTA leaves while the other's copies, products or arrivals reach it
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    } else if (p.split > 1) {
         __syncwarp();
         if (warp < 2) {
             cluster_arrive();
@@ -550,7 +632,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tbase, p.tmem_cols);
+        if constexpr (TWO) tmem_dealloc2(tbase, p.tmem_cols);
+        else tmem_dealloc(tbase, p.tmem_cols);
     }
 }
 
@@ -567,30 +650,30 @@ static int dense_sms() {
 }
 
 // Instruction descriptor: D f32, A and B both fp16 or both bf16, each K- or
-// MN-major, M = 128, N = bn.
-static uint32_t dense_idesc(int bf16, int a_mn, int b_mn, int bn) {
+// MN-major, M = rows, N = bn.
+static uint32_t dense_idesc(int bf16, int a_mn, int b_mn, int rows, int bn) {
     const uint32_t t = bf16 ? 1u : 0u;
     return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-           (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kDtRows >> 4) << 24);
+           (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(rows >> 4) << 24);
 }
 
-template <bool SWAP>
+template <bool SWAP, bool TWO>
 static cudaError_t dense_configure() {
     static std::atomic<bool> configured[64];     // set once per device (a repeat is harmless)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(dense_tc_kernel<SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtSmemMax + 1024);
+        e = cudaFuncSetAttribute(dense_tc_kernel<SWAP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtSmemMax + 1024);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
     }
     return cudaSuccess;
 }
 
-template <bool SWAP>
+template <bool SWAP, bool TWO>
 static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStream_t s) {
-    const cudaError_t e = dense_configure<SWAP>();
+    const cudaError_t e = dense_configure<SWAP, TWO>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -601,12 +684,12 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(TWO ? 2 : p.split);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP>, p);
+    cfg.numAttrs = TWO || p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP, TWO>, p);
 }
 
 // Clusters of `split` CTAs (with a whole SM's shared memory each) that run at
@@ -618,7 +701,7 @@ static int max_clusters(int split) {
     const int at = split == 2 ? 1 : split == 4 ? 2 : 3;
     int n = known[dev][at].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    if (dense_configure<false>() != cudaSuccess) return 0;
+    if (dense_configure<false, false>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(split));
     cfg.blockDim = dim3(kDtThreads);
@@ -630,7 +713,7 @@ static int max_clusters(int split) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, dense_tc_kernel<false>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, dense_tc_kernel<false, false>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return 0;
     }
@@ -638,13 +721,17 @@ static int max_clusters(int split) {
     return n;
 }
 
+struct DensePlan {
+    int bn, split, two;
+};
+
 // Columns of a tile and split of c, by an estimate in SM cycles of a CTA's
 // work: a slice of c takes bn * 2 cycles of the tensor core or its bytes at 66
 // bytes a cycle (what one SM was seen to draw from L2: 0.385 us for the 48 KB
 // of a 256-column slice), whichever is longer; a wave of tiles takes its
 // slices, and the last one an epilogue; all of it at least the operands' bytes
 // at the measured copy rate (23 bytes a cycle and SM).
-static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, int* bn_out, int* split_out) {
+static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePlan* plan) {
     double best = -1.0, dram = 0.0;
     int qmax = 0, kmax = 0;
     double P[2], Q[2], kblocks[2];
@@ -678,8 +765,28 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, int* bn
                                 (split > 1 ? 1500.0 + 100.0 * split : 0.0);
             if (best < 0.0 || cost < best) {
                 best = cost;
-                *bn_out = bn;
-                *split_out = split;
+                *plan = DensePlan{bn, split, 0};
+            }
+        }
+    }
+    if (!swap && qmax > 128) {
+        // pairs of CTAs: 256 x 256 tiles, each CTA bringing half of either operand
+        // (32 KB a slice against the tensor cores' 512 cycles)
+        const int pairs = max_clusters(2);
+        double tiles = 0.0, slices = 0.0, longest = 0.0;
+        for (int i = 0; i < n; ++i) {
+            const double t = std::ceil(P[i] / 256.0) * std::ceil(Q[i] / 256.0);
+            tiles += t;
+            slices += t * kblocks[i];
+            longest = std::max(longest, kblocks[i]);
+        }
+        if (pairs > 0) {
+            const double waves = std::ceil(tiles / pairs);
+            const double work = waves == 1.0 ? longest : std::max(longest, waves * slices / tiles);
+            const double cost = std::max(dram, (work + 0.5 * waves) * 512.0) + 8.0 * 256 + 500.0;
+            if (cost < best) {
+                best = cost;
+                *plan = DensePlan{256, 1, 1};
             }
         }
     }
@@ -712,7 +819,13 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     }
     const DenseGemm& g = gs[0];
     const int sms = dense_sms();
-    dense_plan(gs, n, swap, sms, &p.bn, &p.split);
+    DensePlan plan{};
+    dense_plan(gs, n, swap, sms, &plan);
+    p.bn = plan.bn;
+    p.split = plan.split;
+    p.two = plan.two;
+    const int tile_rows = p.two ? 2 * kDtRows : kDtRows;
+    const int slots = p.two ? max_clusters(2) : sms;         // tiles at work at once
     int live = 0;
     for (int i = 0; i < n; ++i)
         if (p.prob[i].y) {
@@ -730,17 +843,18 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     int kper = 0;
     for (int i = 0; i < n; ++i) {
         DenseProb& d = p.prob[i];
-        d.tiles_p = (d.P + kDtRows - 1) / kDtRows;
+        d.tiles_p = (d.P + tile_rows - 1) / tile_rows;
         d.tiles_q = (d.Q + p.bn - 1) / p.bn;
         const long long t = static_cast<long long>(d.tiles_p) * d.tiles_q;
         if ((tiles += t) > 0x3FFFFFFF) return fail(MILO_ERR_UNSUPPORTED_SHAPE, std::string(what) + ": too many tiles");
         d.tiles = static_cast<int>(t);
-        d.idesc = dense_idesc(p.bf16, d.a_mn, d.b_mn, p.bn);
+        d.idesc = dense_idesc(p.bf16, d.a_mn, d.b_mn, p.two ? 2 * kDtRows : kDtRows, p.bn);
         kper = std::max(kper, (d.kblocks + p.split - 1) / p.split);
     }
     p.tiles = static_cast<int>(tiles);
-    p.bufs = p.split == 1 && p.tiles > sms ? 2 : 1;
-    p.stage_bytes = kDtAtom + p.bn * 128;
+    p.bufs = p.split == 1 && p.tiles > slots ? 2 : 1;
+    const int b_rows = p.two ? p.bn / 2 : p.bn;              // of B per CTA
+    p.stage_bytes = kDtAtom + b_rows * 128;
     // shared memory: the ring (then a split's partial blocks), the row form's
     // staging and bias, barriers
     p.staging = swap ? 0 : 32 * dense_pitch(g.y_dt == MILO_F32 ? 4 : 2);
@@ -752,9 +866,14 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     p.off_staging = std::max(p.stages * p.stage_bytes, part);
     p.off_bias = p.off_staging + staging;
     p.off_bar = p.off_bias + bias;
-    const int smem = p.off_bar + 512 + 1024;
     p.tmem_cols = 32;
     while (p.tmem_cols < static_cast<uint32_t>(p.bufs * p.bn)) p.tmem_cols *= 2;
+    // A CTA takes at least its columns' share of the SM's shared memory, so CTAs
+    // that run side by side never ask for more than the SM's 512 columns: an
+    // allocation that waited while its cluster's other CTAs hold theirs could
+    // wait for ever on a cluster of another stream in the same position.
+    const int smem = std::max(p.off_bar + 512 + 1024,
+                              static_cast<int>(p.tmem_cols) * ((kDtSmemMax + 1024) / 512));
     p.bias = g.bias;
     p.residual = g.residual;
     p.z = g.z;
@@ -771,11 +890,13 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
                                 : make_map(&d.a_map, a[i], dt, d.C, d.P, lda[i] * 2, kDtK, kDtRows, what, swz);
         if (st != MILO_OK) return st;
         st = d.b_mn ? make_map(&d.b_map, b[i], dt, d.Q, d.C, ldb[i] * 2, 64, kDtK, what, swz)
-                    : make_map(&d.b_map, b[i], dt, d.C, d.Q, ldb[i] * 2, kDtK, p.bn, what, swz);
+                    : make_map(&d.b_map, b[i], dt, d.C, d.Q, ldb[i] * 2, kDtK, b_rows, what, swz);
         if (st != MILO_OK) return st;
     }
+    if (p.two) return check_cuda(launch_dense_tc<false, true>(p, 2 * std::min(p.tiles, slots), smem, s), what);
     const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
-    return check_cuda(swap ? launch_dense_tc<true>(p, grid, smem, s) : launch_dense_tc<false>(p, grid, smem, s), what);
+    return check_cuda(swap ? launch_dense_tc<true, false>(p, grid, smem, s) : launch_dense_tc<false, false>(p, grid, smem, s),
+                      what);
 }
 
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
@@ -790,10 +911,10 @@ milo_status launch_dense_pair(const DenseGemm& g0, const DenseGemm& g1, const ch
     if (!g0.y && !g1.y) return MILO_OK;
     // one launch unless the two want different tiles or splits by more than a
     // second launch costs (about 4000 cycles)
-    int bn, split;
+    DensePlan plan;
     const int sms = dense_sms();
-    const double apart = dense_plan(&g0, 1, false, sms, &bn, &split) + dense_plan(&g1, 1, false, sms, &bn, &split) + 4000.0;
-    if (dense_plan(gs, 2, false, sms, &bn, &split) <= apart) return launch_dense(gs, 2, false, what, s);
+    const double apart = dense_plan(&g0, 1, false, sms, &plan) + dense_plan(&g1, 1, false, sms, &plan) + 4000.0;
+    if (dense_plan(gs, 2, false, sms, &plan) <= apart) return launch_dense(gs, 2, false, what, s);
     milo_status r = g0.y ? launch_dense(&g0, 1, false, what, s) : MILO_OK;
     if (r == MILO_OK && g1.y) r = launch_dense(&g1, 1, false, what, s);
     return r;

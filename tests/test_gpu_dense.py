@@ -85,6 +85,53 @@ def test_backward(milo, M, N, K, dt, dyt, act):
         assert torch.equal(milo.milo_dense_linear_backward(dy, x, W, act, z, need=(name,))[name], g[name]), name
 
 
+# tiles of pairs of CTAs (256 x 256), more tiles than fit at once, ragged on every side
+LARGE = [(2600, 2312, 648), (1537, 5000, 264), (4100, 1032, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("dt,out,act,res", [("bf16", "bf16", "gelu_tanh", True), ("f16", "f32", "none", False)])
+def test_large_products(milo, M, N, K, dt, out, act, res):
+    rng = np.random.default_rng(M + N + K)
+    x, W = rand(rng, (M, K), dt), rand(rng, (N, K), dt, K ** -0.5)
+    b, r = rand(rng, (N,), dt), rand(rng, (M, N), out) if res else None
+    zt = torch.empty((M, N), dtype=DT[dt], device="cuda")
+    st = milo.new_status()
+    y = milo.milo_dense_linear(x, W, b, act, r, out_dtype=DT[out], z=zt, dev_status=st)
+    yr, yb, zr, zb = R.linear(n64(x), n64(W), n64(b), act, n64(r) if res else None, dt, out)
+    check(y, yr, yb, "y")
+    check(zt, zr, zb, "z")
+    dy = rand(rng, (M, N), dt, N ** -0.5)
+    g = milo.milo_dense_linear_backward(dy, x, W, act, zt, dev_status=st)
+    want = R.linear_backward(n64(dy), n64(x), n64(W), act, n64(zt), dt, act == "none")
+    for name in g:
+        check(g[name], *want[name], name)
+        one = milo.milo_dense_linear_backward(dy, x, W, act, zt, need=(name,), dev_status=st)[name]
+        assert torch.equal(one, g[name]), name
+    assert int(st.item()) == 0
+
+
+def test_calls_on_several_streams_at_once(milo):
+    """Products of every kind (streamed, split over clusters, pairs of CTAs, both
+    gradients) side by side on four streams give what they give alone."""
+    rng = np.random.default_rng(10)
+    work = []
+    for M, N, K in ((1, 512, 4096), (40, 512, 2048), (700, 64, 2048), (512, 1024, 1024), (2300, 2312, 264)):
+        x, W, dy = rand(rng, (M, K), "bf16"), rand(rng, (N, K), "bf16"), rand(rng, (M, N), "bf16")
+        work.append((x, W, dy, milo.milo_dense_linear(x, W), milo.milo_dense_linear_backward(dy, x, W)))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 4]):
+            x, W, dy, y, g = work[(i * 7) % len(work)]
+            got.append((milo.milo_dense_linear(x, W), y))
+            g2 = milo.milo_dense_linear_backward(dy, x, W)
+            got += [(g2[n], g[n]) for n in g]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
 def test_activations_far_out(milo, act):
     """Pre-activations from 2^-20 to 2^12 and zeros, through an identity weight:
