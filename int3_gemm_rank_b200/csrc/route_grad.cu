@@ -26,69 +26,91 @@ struct RouteGradArgs {
 //     full softmax:  dl[e] = [e = e_j] w_j dw_j - p_e s,  p = softmax(l)
 // (the Jacobian of a softmax q is q_i ([i = l] - q_l); the renormalised one
 // runs over the picked experts only).  L lanes share a token, eight experts
-// each, so a warp takes 32 / L tokens and every reduction has log2 L steps:
-// the instructions, not the bytes, bound a warp that gives a whole token to
-// its 32 lanes (65536 x 64, k 6: 18.7 us that way).  The k <= KM picks are few
-// and read by all L lanes (one L1 line) before anything else, each lane adding
-// those that are its own.
+// and every L-th pick each, so a warp takes 32 / L tokens and every reduction
+// has log2 L steps; the picks meet their experts in shared memory.  The
+// instructions, not the bytes, bound this: 65536 x 64, k 6, took 18.7 us with
+// a warp per token and 11 us with the picks compared in registers.
 template <typename TO, int L, int KM, bool VEC>
 __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradArgs p) {
+    constexpr int kTok = kRgThreads / L, kRow = 8 * L + 4;
+    constexpr int kPicks = (KM + L - 1) / L;              // of a lane
+    __shared__ __align__(16) float rows[kTok][kRow];
     grid_dep_launch();
     grid_dep_wait();
-    const long long i = static_cast<long long>(blockIdx.x) * kRgThreads + threadIdx.x;
-    const bool in = i / L < p.T;                          // the last warp may be part empty
-    const long long t = in ? i / L : p.T - 1;
+    const int lane = threadIdx.x & 31, sub = threadIdx.x % L;
+    const long long i = static_cast<long long>(blockIdx.x) * kTok + threadIdx.x / L;
+    const bool in = i < p.T;                              // the last block may be part empty
+    const long long t = in ? i : p.T - 1;
     const int E = p.E, k = p.k;
     // the lane's experts: eight in a row, or every L-th where rows do not start on
     // 16-byte boundaries
     constexpr int step = VEC ? 1 : L;
-    const int e0 = static_cast<int>(i % L) * (VEC ? 8 : 1);
+    const int e0 = sub * (VEC ? 8 : 1);
     int32_t st = 0;
-    float v[8], wj[KM], dj[KM];
-    int id[KM];
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-        id[j] = -1;
-        wj[j] = dj[j] = 0.0f;
-        if (j < k) {
-            id[j] = p.ids[t * k + j];
-            wj[j] = p.w[t * k + j];
-            dj[j] = p.dw[t * k + j];
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-    if (!p.renorm) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = -INFINITY;
-        const uint16_t* l = p.logits + t * E + e0;
-        if constexpr (VEC) {
-            if (e0 < E) load8<__half>(l, v);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (e0 + q * step < E) v[q] = __half2float(__ushort_as_half(l[q * step]));
-        }
-    }
+    float v[8], g[kPicks], wj[kPicks];
+    int id[kPicks];
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < KM; ++j)
+    for (int r = 0; r < kPicks; ++r) {
+        const int j = sub + r * L;
+        id[r] = -1;
+        g[r] = wj[r] = 0.0f;
         if (j < k) {
-            if (id[j] < 0 || id[j] >= E) st |= MILO_DEV_BAD_EXPERT_ID;
-            else s = fmaf(wj[j], dj[j], s);
+            id[r] = p.ids[t * k + j];
+            wj[r] = p.w[t * k + j];
+            g[r] = p.dw[t * k + j];
+            if (id[r] < 0 || id[r] >= E) {
+                st |= MILO_DEV_BAD_EXPERT_ID;
+                id[r] = -1;
+                g[r] = wj[r] = 0.0f;
+            }
         }
+    }
     if (!p.renorm) {
+        const uint16_t* l = p.logits + t * E + e0;
+        if constexpr (VEC) {
+            if (e0 < E) {
+                load8<__half>(l, v);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = e0 + q * step < E ? __half2float(__ushort_as_half(l[q * step])) : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kPicks; ++r) {
+        g[r] *= wj[r];
+        s += g[r];
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (p.renorm) {
+#pragma unroll
+        for (int r = 0; r < kPicks; ++r) g[r] -= wj[r] * s;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+    } else {
+        bool ok = true;
         float m = -INFINITY, den = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (!isfinite(v[q]) && e0 + q * step < E) st |= MILO_DEV_NONFINITE;
-            m = fmaxf(m, v[q]);                           // NaN counts as -inf, as in milo_route
+            ok = ok && (fabsf(v[q]) <= 65504.0f || e0 + q * step >= E);
+            m = fmaxf(m, v[q]);                           // a NaN counts as -inf, as in milo_route
+        }
+        if (!ok) {
+            st |= MILO_DEV_NONFINITE;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (v[q] != v[q]) v[q] = -INFINITY;
         }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            v[q] = v[q] == v[q] ? expf(v[q] - m) : 0.0f;
+            v[q] = __expf(v[q] - m);
             den += v[q];
         }
 #pragma unroll
@@ -97,22 +119,47 @@ __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradA
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] *= c;
     }
-#pragma unroll
-    for (int j = 0; j < KM; ++j)
-        if (j < k) {
-            const float g = p.renorm ? wj[j] * (dj[j] - s) : wj[j] * dj[j];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (id[j] == e0 + q * step) v[q] += g;
-        }
-    if (!in) return;
-    TO* d = static_cast<TO*>(p.dl) + t * E + e0;
+    float* row = rows[threadIdx.x / L];
     if constexpr (VEC) {
-        if (e0 < E) store8<TO>(d, v, st);
+        reinterpret_cast<float4*>(row + e0)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(row + e0)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (e0 + q * step < E) d[q * step] = from_f32<TO>(v[q], st);
+        for (int q = 0; q < 8; ++q) row[e0 + q * step] = v[q];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kPicks; ++r) {
+        // picks of a token are distinct (milo_route's); two alike would be added one
+        // after the other, lowest first
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, id[r] >= 0 ? (lane / L) << 16 | id[r] : -1 - lane);
+        unsigned left = same;
+        bool mine = __ffs(left) - 1 == lane;
+        while (true) {
+            if (mine && id[r] >= 0) row[id[r]] += g[r];
+            __syncwarp();
+            left &= left - 1;
+            if (!__any_sync(0xFFFFFFFFu, left != 0)) break;
+            mine = left != 0 && __ffs(left) - 1 == lane;
+        }
+    }
+    if constexpr (VEC) {
+        const float4 a = reinterpret_cast<const float4*>(row + e0)[0], b = reinterpret_cast<const float4*>(row + e0)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = row[e0 + q * step];
+    }
+    if (in) {
+        TO* d = static_cast<TO*>(p.dl) + t * E + e0;
+        if constexpr (VEC) {
+            if (e0 < E) store8<TO>(d, v, st);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (e0 + q * step < E) d[q * step] = from_f32<TO>(v[q], st);
+        }
     }
     flag(p.dev_status, st);
 }

@@ -248,6 +248,28 @@ def test_route_backward_extremes(milo):
     assert int(st.item()) & milo.MILO_DEV_NONFINITE
 
 
+def test_route_backward_of_repeated_picks(milo):
+    """Ids a caller made up: a token's two or three picks of one expert add up,
+    in the same bits every time."""
+    rng = np.random.default_rng(14)
+    T, E, k = 70, 12, 5
+    ids = torch.from_numpy(rng.integers(0, E, (T, k)).astype(np.int32)).cuda()
+    ids[3] = 7
+    r = {"ids": ids, "w": rand(rng, (T, k), "f32")}
+    dw = rand(rng, (T, k), "f32")
+    logits = rand(rng, (T, E), "f16")
+    dl = milo.milo_route_backward(r, dw, False, E, logits, out_dtype=torch.float32)
+    lg, w = n64(logits), n64(r["w"])
+    p = np.exp(lg - lg.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    want = -p * (w * n64(dw)).sum(1, keepdims=True)
+    np.add.at(want, (np.arange(T)[:, None], ids.cpu().numpy()), w * n64(dw))
+    mag = np.abs(w * n64(dw)).sum(1, keepdims=True) + 0 * want
+    check(dl, want, 2.0 ** -17 * mag, "repeated")
+    for _ in range(3):
+        assert torch.equal(milo.milo_route_backward(r, dw, False, E, logits, out_dtype=torch.float32), dl)
+
+
 def test_chain_around_the_grouped_linear(milo):
     """route -> dispatch -> grouped int3 product over the grouped rows ->
     combine: the slots' rows are bit for bit those of the ungrouped call, and
