@@ -695,11 +695,10 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
 // Clusters of `split` CTAs (with a whole SM's shared memory each) that run at
 // once on the current device; asked once per device and size.
 static int max_clusters(int split) {
-    static std::atomic<int> known[64][4];
+    static std::atomic<int> known[64][kDtMaxSplit + 1];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    const int at = split == 2 ? 1 : split == 4 ? 2 : 3;
-    int n = known[dev][at].load(std::memory_order_relaxed);
+    int n = known[dev][split].load(std::memory_order_relaxed);
     if (n > 0) return n;
     if (dense_configure<false, false>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
@@ -717,7 +716,7 @@ static int max_clusters(int split) {
         cudaGetLastError();
         return 0;
     }
-    known[dev][at].store(n, std::memory_order_relaxed);
+    known[dev][split].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -747,7 +746,7 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePl
     for (int bn = swap ? bn_swap : 64; bn <= (swap ? bn_swap : 256); bn += 64) {
         if (!swap && bn > 64 && bn - 64 >= qmax) break;          // the tile would be part empty
         const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 66.0);
-        for (int split = 1; split <= kDtMaxSplit && (split == 1 || kmax >= 2 * split); split *= 2) {
+        for (int split = 1; split <= kDtMaxSplit && (split == 1 || kmax >= 2 * split); ++split) {
             double tiles = 0.0, slices = 0.0, longest = 0.0;
             for (int i = 0; i < n; ++i) {
                 const double t = std::ceil(P[i] / 128.0) * std::ceil(Q[i] / static_cast<double>(bn));

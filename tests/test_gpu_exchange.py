@@ -264,6 +264,7 @@ def test_route_backward_of_repeated_picks(milo):
     p /= p.sum(1, keepdims=True)
     want = -p * (w * n64(dw)).sum(1, keepdims=True)
     np.add.at(want, (np.arange(T)[:, None], ids.cpu().numpy()), w * n64(dw))
+    # as R.route_backward: (k + 4) 2^-24 of the terms and 2^-18 + E 2^-24 of p |s|, all at most mag
     mag = np.abs(w * n64(dw)).sum(1, keepdims=True) + 0 * want
     check(dl, want, 2.0 ** -17 * mag, "repeated")
     for _ in range(3):
