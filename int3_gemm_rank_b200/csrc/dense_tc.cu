@@ -63,16 +63,19 @@ constexpr int dense_pitch(int esize) { return 32 * esize + 16; }
 // One product of a launch.
 struct DenseProb {
     CUtensorMap a_map, b_map;
+    CUtensorMap y_map;                       // set when `store`
     int P, Q, C;
     int a_mn, b_mn;
     int kblocks;                             // slices of 64 c
     int tiles_p, tiles_q, tiles;
     uint32_t idesc;
     int vec;                                 // 16-byte output rows
+    int store;                               // ... and no residual: blocks of y (and z) leave by TMA
     void* y;                                 // [P, Q] (SWAP: [Q, P])
 };
 
 struct DenseTc {
+    CUtensorMap z_map;
     DenseProb prob[2];                       // one product, or two that share the grid (a layer's dx and dW)
     int tiles;                               // of both
     int bf16, bn, stages, split;             // columns of a tile; CTAs that share a tile's c
@@ -80,6 +83,7 @@ struct DenseTc {
     uint32_t tmem_cols;
     int bufs;                                // accumulators in TMEM (2: persistent)
     int stage_bytes, staging, off_staging, off_bias, off_bar;
+    int out_bufs, out_bytes;                 // TMA store: buffers of an epilogue warp, bytes of one
     // epilogue (residual and z as y; SWAP: p is the feature)
     const void *bias, *residual;
     void* z;
@@ -275,8 +279,53 @@ __device__ __forceinline__ void dense_add(const DenseTc& p, const DenseProb& d, 
     __syncwarp();
 }
 
-__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg, const float* bias,
-                                                  int p0, int q0, int lane, int32_t& st) {
+// Which of the warp's TMA store buffers comes next.
+struct DenseOut {
+    uint8_t* stg;
+    int next;
+};
+
+// The warp's 32 x 32 block to rows p0.., columns q0.. by a TMA store, which cuts
+// what lies outside: the lane's row into a buffer in the map's swizzled layout
+// (64-byte rows: 16-byte piece c at c ^ ((row / 2) % 4); 128-byte rows: c ^ (row
+// % 8), so that eight lanes' pieces fall on different banks), one copy out.
+template <int DT>
+__device__ __forceinline__ void dense_tma_put(const DenseTc& p, const CUtensorMap* map, const float (&v)[32], DenseOut& o,
+                                              int p0, int q0, int lane, int32_t& st) {
+    if (lane == 0) {
+        // the buffer's last copy has read it
+        if (p.out_bufs == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    __syncwarp();
+    uint8_t* buf = o.stg + o.next * p.out_bytes;
+    if constexpr (DT == MILO_F32) {
+        uint8_t* row = buf + lane * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack16<DT>(v[2 * i], v[2 * i + 1]);
+        if constexpr (DT == MILO_F16) half_range(v, w, st);
+        uint8_t* row = buf + lane * 64;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(row + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+            "cp.async.bulk.commit_group;"
+            ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(buf)), "r"(q0), "r"(p0) : "memory");
+    if (p.out_bufs == 2) o.next ^= 1;
+}
+
+__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], DenseOut& o,
+                                                  const float* bias, int p0, int q0, int lane, int32_t& st) {
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -287,15 +336,21 @@ __device__ __forceinline__ void dense_store_chunk(const DenseTc& p, const DenseP
             v[4 * i + 3] += t.w;
         }
     }
-    if (p.z) {
-        if (p.bf16) dense_put<MILO_BF16>(p, d, p.z, v, stg, p0, q0, lane, st);
-        else dense_put<MILO_F16>(p, d, p.z, v, stg, p0, q0, lane, st);
-    }
+    if (p.z)
+        with_dtype(p.bf16 ? MILO_BF16 : MILO_F16, [&](auto dt) {
+            constexpr int DT = decltype(dt)::value;
+            if (d.store) dense_tma_put<DT>(p, &p.z_map, v, o, p0, q0, lane, st);
+            else dense_put<DT>(p, d, p.z, v, o.stg, p0, q0, lane, st);
+        });
     act_tile(p.act, v);
     with_dtype(p.y_dt, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (p.residual) dense_add<DT>(p, d, v, stg, p0, q0, lane);
-        dense_put<DT>(p, d, d.y, v, stg, p0, q0, lane, st);
+        if (d.store) {
+            dense_tma_put<DT>(p, &d.y_map, v, o, p0, q0, lane, st);
+        } else {
+            if (p.residual) dense_add<DT>(p, d, v, o.stg, p0, q0, lane);
+            dense_put<DT>(p, d, d.y, v, o.stg, p0, q0, lane, st);
+        }
     });
 }
 
@@ -405,7 +460,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     // epilogue warps: lane quarter, which half of the column blocks, own buffers
     const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
-    uint8_t* stg = smem + p.off_staging + ew * p.staging;
+    DenseOut out{smem + p.off_staging + ew * p.staging, 0};
     float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + ew * kDtBias;
 
     if (warp == 0) {
@@ -541,7 +596,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
                 if (p0 >= d.P || q0 + c >= d.Q) continue;
                 if constexpr (SWAP) dense_store_swapped(p, d, v, p0, q0 + c, lane, st_bits);
-                else dense_store_chunk(p, d, v, stg, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
+                else dense_store_chunk(p, d, v, out, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
             }
             tc_fence_before();
             __syncwarp();
@@ -622,11 +677,13 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                         sbias[lane] = q0 + lane < d.Q ? load16(p.bias, q0 + lane, p.bf16) : 0.0f;
                         __syncwarp();
                     }
-                    dense_store_chunk(p, d, v, stg, sbias, p0, q0, lane, st_bits);
+                    dense_store_chunk(p, d, v, out, sbias, p0, q0, lane, st_bits);
                 }
             }
         }
     }
+    // the stores have left shared memory and reached the outputs
+    if (!SWAP && warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     flag(p.dev_status, st_bits);
     tc_fence_before();
     __syncthreads();
@@ -815,6 +872,7 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
         d.kblocks = (d.C + kDtK - 1) / kDtK;
         d.y = g.y;
         d.vec = g.Q % 8 == 0 && aligned(g.y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
+        d.store = !swap && d.vec && !g.residual;
     }
     const DenseGemm& g = gs[0];
     const int sms = dense_sms();
@@ -855,13 +913,27 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     const int b_rows = p.two ? p.bn / 2 : p.bn;              // of B per CTA
     p.stage_bytes = kDtAtom + b_rows * 128;
     // shared memory: the ring (then a split's partial blocks), the row form's
-    // staging and bias, barriers
-    p.staging = swap ? 0 : 32 * dense_pitch(g.y_dt == MILO_F32 ? 4 : 2);
-    const int staging = kDtEpiWarps * p.staging, bias = swap ? 0 : kDtEpiWarps * kDtBias * 4;
+    // output buffers and bias, barriers
+    // (TMA stores from two buffers a warp where that costs the ring no stage of
+    // the four or more that keep it full)
+    const int es = g.y_dt == MILO_F32 ? 4 : 2, bias = swap ? 0 : kDtEpiWarps * kDtBias * 4;
+    const int want = std::max(2, p.bufs == 2 ? kDtMaxStages : kper);
+    bool store = !swap;
+    for (int i = 0; i < n; ++i) store = store && p.prob[i].store;
+    for (int i = 0; i < n; ++i) p.prob[i].store = store;
+    p.out_bytes = 32 * 32 * es;
+    auto ring = [&](int staging) { return std::min({kDtMaxStages, (kDtSmemMax - kDtEpiWarps * staging - bias - 512) / p.stage_bytes, want}); };
+    p.out_bufs = 1;
+    p.staging = swap ? 0 : store ? p.out_bytes : 32 * dense_pitch(es);
+    p.stages = ring(p.staging);
+    if (store && ring(2 * p.out_bytes) >= std::min(p.stages, 4)) {
+        p.out_bufs = 2;
+        p.staging = 2 * p.out_bytes;
+        p.stages = ring(p.staging);
+    }
+    const int staging = kDtEpiWarps * p.staging;
     const int w = swap ? 16 : kDtChunk;
     const int part = p.split > 1 ? static_cast<int>(round_up(4 * (p.bn / w), p.split)) * w * 128 : 0;
-    p.stages = std::min({kDtMaxStages, (kDtSmemMax - staging - bias - 512) / p.stage_bytes,
-                         std::max(2, p.bufs == 2 ? kDtMaxStages : kper)});
     p.off_staging = std::max(p.stages * p.stage_bytes, part);
     p.off_bias = p.off_staging + staging;
     p.off_bar = p.off_bias + bias;
@@ -890,6 +962,13 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
         if (st != MILO_OK) return st;
         st = d.b_mn ? make_map(&d.b_map, b[i], dt, d.Q, d.C, ldb[i] * 2, 64, kDtK, what, swz)
                     : make_map(&d.b_map, b[i], dt, d.C, d.Q, ldb[i] * 2, kDtK, b_rows, what, swz);
+        if (st != MILO_OK) return st;
+        if (!d.store) continue;
+        // output blocks of 32 x 32
+        st = make_map(&d.y_map, d.y, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt, d.Q, d.P, static_cast<uint64_t>(d.Q) * es,
+                      32, 32, what, es == 4 ? swz : CU_TENSOR_MAP_SWIZZLE_64B);
+        if (st == MILO_OK && i == 0 && p.z)
+            st = make_map(&p.z_map, p.z, dt, d.Q, d.P, static_cast<uint64_t>(d.Q) * 2, 32, 32, what, CU_TENSOR_MAP_SWIZZLE_64B);
         if (st != MILO_OK) return st;
     }
     if (p.two) return check_cuda(launch_dense_tc<false, true>(p, 2 * std::min(p.tiles, slots), smem, s), what);
