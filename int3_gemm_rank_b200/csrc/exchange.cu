@@ -7,7 +7,10 @@
 // t*k + j the flat slot of token t's j-th pick and p = inv_perm[f] its row in
 // expert order: xs[p] = w[f] x[t] (w optional).  The kernel walks the tokens,
 // not the expert rows, so it reads each token row once for its k copies.
-// Bound by memory: T H elements read, T k H written.
+// Bound by memory: T H elements read, T k H written.  Measured (B200, bf16):
+// 8192 x 2048, k 6, 39.4 us = 0.91 of the measured copy rate; 8192 x 4096, k 2,
+// 37.9 us = 0.81 (four groups of columns a thread 39.5, the rows through
+// shared memory 37.9 and, k 6, 46).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -21,6 +21,13 @@
 // A row that starts off a 16-byte boundary comes in the aligned pieces that
 // cover it; its columns are then read one element per lane (lane, lane + 32,
 // ...), which no misalignment slows down, and written the same way.
+//
+// Measured (B200, device time, of the measured copy rate): combine 8192 x 2048,
+// k 6, bf16 with a residual 42.3 us (0.97; 54 with 8 warps a block, 48 with
+// 16); dispatch's gradient 8192 x 4096, k 2, bf16 31.6 us (0.97); combine's
+// gradient 5003 x 2048, k 6, fp16 47 us (0.82), and at width 2051 75 us
+// (0.52), where the one-element reads and stores bound it.  Threads that load
+// the rows into registers reached 0.62 of the rate at best.
 #pragma once
 
 #include <algorithm>

@@ -23,11 +23,16 @@ SLOPE = 1.13
 _erf = np.vectorize(math.erf, otypes=[np.float64])
 
 
+def _sigmoid(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
+
+
 def act(name, z):
     if name == "relu":
         return np.maximum(z, 0.0)
     if name == "silu":
-        return z / (1.0 + np.exp(-z))
+        return z * _sigmoid(z)
     if name == "gelu":
         return 0.5 * z * (1.0 + _erf(z / math.sqrt(2.0)))
     if name == "gelu_tanh":
@@ -39,7 +44,7 @@ def dact(name, z):
     if name == "relu":
         return (z > 0).astype(np.float64)
     if name == "silu":
-        g = 1.0 / (1.0 + np.exp(-z))
+        g = _sigmoid(z)
         return g * (1.0 + z * (1.0 - g))
     if name == "gelu":
         return 0.5 * (1.0 + _erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)

@@ -169,6 +169,66 @@ def test_in_place_residual_views_and_an_empty_batch(milo):
     assert g["dx"].shape == (0, 128) and not g["dW"].any() and not g["db"].any()
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 24, 131072), (20, 40, 65536), (300, 40, 16384), (700, 130, 520)])
+def test_long_sums_and_fp32_residuals(milo, M, N, K):
+    rng = np.random.default_rng(K)
+    x, W = rand(rng, (M, K), "f16"), rand(rng, (N, K), "f16", K ** -0.5)
+    r, b = rand(rng, (M, N), "f32"), rand(rng, (N,), "f16")
+    z = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    y = milo.milo_dense_linear(x, W, b, "silu", r, z=z)
+    assert y.dtype == torch.float32              # the residual's type
+    yr, yb, zr, zb = R.linear(n64(x), n64(W), n64(b), "silu", n64(r), "f16", "f32")
+    check(y, yr, yb, "y")
+    check(z, zr, zb, "z")
+
+
+def test_outputs_past_32_bits(milo):
+    """M * N above 2^31 elements: the last rows are where they belong."""
+    M, N, K = 40000, 60000, 64
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x = torch.randn((M, K), generator=gen, device="cuda").bfloat16()
+    W = torch.randn((N, K), generator=gen, device="cuda").bfloat16()
+    y = milo.milo_dense_linear(x, W)
+    rows = [0, 1, M // 2, 35792, M - 1]
+    want = x[rows].double() @ W.double().t()
+    bound = R._rounded(n64(want), R._mma(K) * n64(x[rows].double().abs() @ W.double().abs().t()), "bf16")
+    check(y[rows], n64(want), bound, "rows")
+    g = milo.milo_dense_linear_backward(y, x, W, need=("db",))["db"]
+    col = y[:, [0, N - 1]].double()
+    err = (g[[0, N - 1]].double() - col.sum(0)).abs()
+    assert (err <= 2.0 ** -8 * col.sum(0).abs() + M * 2.0 ** -24 * col.abs().sum(0) * 1.01).all()
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured: what the library sets up once
+    (kernel attributes, occupancy) does not disturb the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, int3_gemm_rank_b200 as milo
+x = torch.randn(300, 512, device="cuda").bfloat16(); W = torch.randn(64, 512, device="cuda").bfloat16()
+one = x[:2].clone()
+inv = torch.arange(600, dtype=torch.int32, device="cuda")
+r = {"ids": torch.zeros((300, 2), dtype=torch.int32, device="cuda"), "inv_perm": inv}
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = milo.milo_dense_linear(x, W); s = milo.milo_dense_linear(one, W)
+    b = milo.milo_dense_linear_backward(y, x, W)
+    xs = milo.milo_dispatch(x, r); c = milo.milo_combine(xs, r)
+g.replay(); torch.cuda.synchronize()
+assert torch.equal(y, milo.milo_dense_linear(x, W)) and torch.equal(s, milo.milo_dense_linear(one, W))
+assert torch.equal(b["dW"], milo.milo_dense_linear_backward(y, x, W)["dW"])
+assert torch.equal(c, (x.float() * 2).bfloat16())
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
 def test_nan_and_inf_stay_in_their_rows(milo):
     """A NaN or infinite row of x reaches its own output row only, at sizes with
     ragged tiles."""

@@ -157,6 +157,43 @@ def test_rows_that_start_anywhere(milo, dt, out, H, so, oo):
         assert torch.equal(buf[:oo], before[:oo]) and torch.equal(buf[oo + n * H:], before[oo + n * H:]), name
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [131, 2051])
+def test_residual_in_place_at_odd_widths(milo, dt, H):
+    """Rows whose 16-byte pieces are shared with their neighbours', read and
+    written by different warps."""
+    rng = np.random.default_rng(H)
+    T, k = 900, 3
+    r = make_route(milo, rng, T, k, 8, "none")
+    inv = r["inv_perm"].cpu().numpy().reshape(T, k).astype(int)
+    rows, y = rand(rng, (T * k, H), dt), rand(rng, (T, H), dt)
+    want = R.combine(n64(rows), inv, n64(r["w"]), n64(y), dt)
+    milo.milo_combine(rows, r, r["w"], y, y=y)
+    check(y, *want, "in place")
+
+
+@pytest.mark.parametrize("H", [64, 67])
+def test_weights_of_dropped_slots_do_not_matter(milo, H):
+    rng = np.random.default_rng(15)
+    T, k = 40, 4
+    r = make_route(milo, rng, T, k, 8, "some")
+    inv = r["inv_perm"].cpu().numpy().reshape(T, k).astype(int)
+    w = n64(r["w"])
+    bad = r["w"].clone()
+    bad[torch.from_numpy(inv < 0).cuda()] = float("nan")
+    x, rows = rand(rng, (T, H), "bf16"), rand(rng, (T * k, H), "bf16")
+    zero = torch.zeros((T * k, H), dtype=torch.bfloat16, device="cuda")
+    z64 = np.zeros((T * k, H))
+    check(milo.milo_dispatch(x, r, bad, xs=zero.clone()), *R.dispatch(n64(x), inv, w, "bf16", z64), "dispatch")
+    check(milo.milo_combine(rows, r, bad), *R.combine(n64(rows), inv, w, None, "bf16"), "combine")
+    dx, dw = milo.milo_dispatch_backward(rows, r, x, bad)
+    check(dx, *R.combine(n64(rows), inv, w, None, "bf16"), "dx")
+    check(dw, *R.slot_dots(n64(x), n64(rows), inv), "dw")
+    dys, dw = milo.milo_combine_backward(x, r, rows, bad, dys=zero.clone())
+    check(dys, *R.dispatch(n64(x), inv, w, "bf16", z64), "dys")
+    check(dw, *R.slot_dots(n64(x), n64(rows), inv), "dw")
+
+
 def test_bad_rows_are_flagged_and_skipped(milo):
     rng = np.random.default_rng(8)
     T, k, H = 4, 2, 32
