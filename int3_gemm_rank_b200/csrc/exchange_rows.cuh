@@ -25,8 +25,8 @@
 // Measured (B200, device time, of the measured copy rate): combine 8192 x 2048,
 // k 6, bf16 with a residual 42.3 us (0.97; 54 with 8 warps a block, 48 with
 // 16); dispatch's gradient 8192 x 4096, k 2, bf16 31.6 us (0.97); combine's
-// gradient 5003 x 2048, k 6, fp16 47 us (0.82), and at width 2051 75 us
-// (0.52), where the one-element reads and stores bound it.  Threads that load
+// gradient 5003 x 2048, k 6, fp16 47 us (0.82), and at width 2051 55 us
+// (0.70), where the one-element reads and stores bound it.  Threads that load
 // the rows into registers reached 0.62 of the rate at best.
 #pragma once
 
@@ -50,7 +50,7 @@ constexpr int kXrSmem = 216 * 1024;
 
 struct XRowsParams {
     ExchangeParams x;
-    int cols, nch;              // columns of a piece (a multiple of 64), pieces of a row
+    int cols, nch;              // columns of a piece (a multiple of 64; the last may be up to 64 longer), pieces of a row
     int pitch, nrows;           // bytes between a stage's rows; rows of a stage
     int team;                   // gradients: warps per token
 };
@@ -89,29 +89,29 @@ __device__ __forceinline__ uint32_t row_window(uintptr_t a, uint32_t len, uintpt
 }
 
 // The lane's eight columns of a block of 256 that starts at column v0 of a row
-// in shared memory (m elements in, see row_window); 0 from column nc on.  AL:
-// columns v0 + 8 lane.., else v0 + lane, + 32, ...
-template <typename T, bool AL>
+// in shared memory (m elements in, see row_window); 0 from column nc on (FULL:
+// the block ends before).  AL: columns v0 + 8 lane.., else v0 + lane, + 32, ...
+template <typename T, bool AL, bool FULL>
 __device__ __forceinline__ void read_cols(const uint8_t* row, int m, int v0, int lane, int nc, float (&v)[8]) {
     if constexpr (AL) {
-        if (v0 + 8 * lane < nc) load8<T>(row + (v0 + 8 * lane) * sizeof(T), v);
+        if (FULL || v0 + 8 * lane < nc) load8<T>(row + (v0 + 8 * lane) * sizeof(T), v);
     } else {
         const T* p = reinterpret_cast<const T*>(row) + m + v0 + lane;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = v0 + lane + 32 * q < nc ? to_f32(p[32 * q]) : 0.0f;
+        for (int q = 0; q < 8; ++q) v[q] = FULL || v0 + lane + 32 * q < nc ? to_f32(p[32 * q]) : 0.0f;
     }
 }
 
 // The same columns of a row in global memory (`row` points to column 0 of the piece).
-template <typename T, bool AL>
+template <typename T, bool AL, bool FULL>
 __device__ __forceinline__ void write_cols(T* row, int v0, int lane, int nc, const float (&v)[8], int32_t& st) {
     if constexpr (AL) {
-        if (v0 + 8 * lane < nc) store8<T>(row + v0 + 8 * lane, v, st);
+        if (FULL || v0 + 8 * lane < nc) store8<T>(row + v0 + 8 * lane, v, st);
     } else {
         T e[8];
         to_elems<T>(v, e, st);
         T* d = row + v0 + lane;
-        if (v0 + 256 <= nc) {
+        if (FULL || v0 + 256 <= nc) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) d[32 * q] = e[q];
         } else {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
     Cursor head{kDot ? gw : gw / P.nch, kDot ? g : gw - gw / P.nch * P.nch};
     Cursor tail = head;
     auto issue = [&](int s) {
-        const int c0 = head.ch * P.cols, nc = min(P.cols, p.H - c0);
+        const int c0 = head.ch * P.cols, nc = head.ch == P.nch - 1 ? p.H - c0 : P.cols;
         const int r = lane < p.k ? slot_row(nidx, rows, st) : -1;
         const unsigned mask = __ballot_sync(0xFFFFFFFFu, r >= 0);
         const int pos = __popc(mask & ((1u << lane) - 1u));
@@ -244,15 +244,16 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
             if (++s == kXrStages) { s = 0; phase ^= 1; }
             continue;
         }
-        const int t = tail.t, c0 = tail.ch * P.cols, nc = min(P.cols, p.H - c0);
+        const int t = tail.t, c0 = tail.ch * P.cols, nc = tail.ch == P.nch - 1 ? p.H - c0 : P.cols;
         const uint8_t* stage = ring + s * P.nrows * P.pitch;
         const XMeta* mt = meta[warp][s];
         const int cnt = live[warp][s];
-        for (int v0 = 0; v0 < nc; v0 += 256) {
+        auto block = [&](auto full, int v0) {
+            constexpr bool FULL = decltype(full)::value;
             float a[8], acc[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) a[q] = acc[q] = 0.0f;
-            if (has_tok) read_cols<TT, AL>(stage + tok_at * P.pitch, mt[KM].m, v0, lane, nc, a);
+            if (has_tok) read_cols<TT, AL, FULL>(stage + tok_at * P.pitch, mt[KM].m, v0, lane, nc, a);
             // slots j..j + N - 1 of the live ones
             auto slots = [&](auto count, int j, float* d) {
                 constexpr int N = decltype(count)::value;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
                     x[u] = mt[j + u];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) b[u][q] = 0.0f;
-                    if constexpr (kLoadRows) read_cols<TI, AL>(stage + (j + u) * P.pitch, x[u].m, v0, lane, nc, b[u]);
+                    if constexpr (kLoadRows) read_cols<TI, AL, FULL>(stage + (j + u) * P.pitch, x[u].m, v0, lane, nc, b[u]);
                 }
 #pragma unroll
                 for (int u = 0; u < N; ++u) {
@@ -274,18 +275,29 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
                         else acc[q] = fmaf(x[u].w, b[u][q], acc[q]);
                     }
                     if constexpr (kToRows)
-                        write_cols<TO, AL>(static_cast<TO*>(p.out) + static_cast<long long>(x[u].row) * p.H + c0, v0, lane, nc,
+                        write_cols<TO, AL, FULL>(static_cast<TO*>(p.out) + static_cast<long long>(x[u].row) * p.H + c0, v0, lane, nc,
                                            b[u], st);
                 }
             };
+            if constexpr (FULL || !kDot) {
 #pragma unroll
-            for (int g = 0; g < KM; g += KB) {
-                if (g + KB <= cnt) {
-                    slots(std::integral_constant<int, KB>{}, g, dot + g);
-                } else {
+                for (int g4 = 0; g4 < KM; g4 += KB) {
+                    if (g4 + KB <= cnt) {
+                        slots(std::integral_constant<int, KB>{}, g4, dot + g4);
+                    } else {
 #pragma unroll
-                    for (int u = 0; u < KB - 1; ++u)
-                        if (g + u < cnt) slots(std::integral_constant<int, 1>{}, g + u, dot + g + u);
+                        for (int u = 0; u < KB - 1; ++u)
+                            if (g4 + u < cnt) slots(std::integral_constant<int, 1>{}, g4 + u, dot + g4 + u);
+                    }
+                }
+            } else {
+                // a row's rest: one body for all slots
+#pragma unroll 1
+                for (int j = 0; j < cnt; ++j) {
+                    float d1[1] = {0.0f};
+                    slots(std::integral_constant<int, 1>{}, j, d1);
+#pragma unroll
+                    for (int u = 0; u < KM; ++u) dot[u] += u == j ? d1[0] : 0.0f;
                 }
             }
             if constexpr (!kToRows) {
@@ -293,9 +305,17 @@ __global__ void __launch_bounds__(kXrThreads, 1) exchange_rows_kernel(const XRow
 #pragma unroll
                     for (int q = 0; q < 8; ++q) acc[q] += a[q];
                 }
-                write_cols<TO, AL>(static_cast<TO*>(p.out) + static_cast<long long>(t) * p.H + c0, v0, lane, nc, acc, st);
+                write_cols<TO, AL, FULL>(static_cast<TO*>(p.out) + static_cast<long long>(t) * p.H + c0, v0, lane, nc, acc, st);
             }
-        }
+        };
+        // whole blocks without a test per column, where that is worth a second copy
+        // of the code (combine's gradient at width 2051 55 us against 59; but
+        // misaligned dispatch 53 us with one copy and 65 with two, combine's
+        // gradient at aligned rows 47 and 51)
+        int v0 = 0;
+        if constexpr (MODE != kXDispatch && !(AL && MODE == kXCombineGrad))
+            for (; v0 + 256 <= nc; v0 += 256) block(std::true_type{}, v0);
+        for (; v0 < nc; v0 += 256) block(std::false_type{}, v0);
         if constexpr (kDot) {
             if (tail.ch + team >= P.nch) {
                 // this warp's last piece of the token: the sums over its lanes, to
@@ -383,14 +403,17 @@ inline cudaError_t run_rows(const ExchangeParams& p, bool al, cudaStream_t s) {
     const double rows_moved = (MODE == kXDispatch ? 1 : p.k + 1) + (MODE == kXCombineGrad || MODE == kXDispatch ? p.k : 1);
     const long long nw = 148LL * kXrWarps;
     double best = -1.0;
-    for (int b = std::max(1, max_cols / 256); b >= 1; --b) {
-        const int cols = std::min(max_cols, 256 * b), nch = (p.H + cols - 1) / cols;
+    // a rest of up to 64 columns goes with the last piece where the ring has room
+    const int rest = max_cols >= 320 ? 64 : 0;
+    for (int b = std::max(1, (max_cols - rest) / 256); b >= 1; --b) {
+        const int cols = std::min(max_cols - rest, 256 * b);
+        const int nch = std::max(1, (p.H - rest + cols - 1) / cols);
         for (int team : kXrTeams) {
             if (team > 1 && (!dot || team > nch)) break;
             const long long warps = nw / team;
             const long long items = dot ? (p.T + warps - 1) / warps * ((nch + team - 1) / team)
                                         : (static_cast<long long>(p.T) * nch + nw - 1) / nw;
-            double cost = items * (0.15 + 0.14 * rows_moved * std::min(b, (p.H + 255) / 256));
+            double cost = items * (0.15 + 0.14 * rows_moved * std::min(static_cast<double>(b), p.H / 256.0));
             if (team > 1) cost += 0.2 * ((p.T + warps - 1) / warps);
             if (best < 0.0 || cost < best * 0.999) {
                 best = cost;
@@ -400,7 +423,7 @@ inline cudaError_t run_rows(const ExchangeParams& p, bool al, cudaStream_t s) {
             }
         }
     }
-    P.pitch = P.cols * es + slack;
+    P.pitch = std::min(P.cols + rest, (p.H + 63) / 64 * 64) * es + slack;
     const size_t smem = static_cast<size_t>(kXrWarps) * kXrStages * P.nrows * P.pitch;
     if (MODE != kXDispatch && al) {
         if (p.k <= 2) return launch_rows<TI, TO, MODE != kXDispatch, 2, MODE>(P, smem, s);
