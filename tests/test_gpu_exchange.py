@@ -157,6 +157,16 @@ def test_rows_that_start_anywhere(milo, dt, out, H, so, oo):
         assert torch.equal(buf[:oo], before[:oo]) and torch.equal(buf[oo + n * H:], before[oo + n * H:]), name
 
 
+def test_no_tokens(milo):
+    r = {"ids": torch.empty((0, 2), dtype=torch.int32, device="cuda"), "w": torch.empty((0, 2), device="cuda"),
+         "inv_perm": torch.empty(0, dtype=torch.int32, device="cuda")}
+    x = torch.empty((0, 24), dtype=torch.bfloat16, device="cuda")
+    assert milo.milo_dispatch(x, r).shape == (0, 24) and milo.milo_combine(x, r, r["w"], x).shape == (0, 24)
+    for grads in (milo.milo_dispatch_backward(x, r, x, r["w"]), milo.milo_combine_backward(x, r, x, r["w"])):
+        assert grads[0].shape == (0, 24) and grads[1].shape == (0, 2)
+    assert milo.milo_route_backward(r, r["w"], True, 8).shape == (0, 8)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("H", [131, 2051])
 def test_residual_in_place_at_odd_widths(milo, dt, H):
