@@ -497,11 +497,13 @@ def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, log
     is the dict milo_route returned for fp16 `logits` [T, E] with the same
     `renorm`; a renormalised gradient does not need the logits."""
     ids, w = route["ids"], route["w"]
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError("route['ids'] must be [T, k]")
     dev = ids.device
-    T, k = ids.shape
-    _arg(ids, "route['ids']", (torch.int32,))
+    T, k = shape
+    if not (ids.dtype is torch.int32 and ids.is_cuda and ids.is_contiguous()):
+        _arg(ids, "route['ids']", (torch.int32,))
     _need(w, "route['w']", (torch.float32,), (T, k), dev)
     _need(dw, "dw", (torch.float32,), (T, k), dev)
     if logits is not None:
@@ -519,9 +521,11 @@ def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, log
 # token rows in expert order
 # ---------------------------------------------------------------------------
 
-# The current stream's handle without building a Stream object (it costs
-# microseconds, as much as a small kernel).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and stream without building Device and Stream objects (a
+# Stream costs microseconds, as much as a small kernel).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _p(t):
@@ -530,13 +534,14 @@ def _p(t):
 
 def _launch(dev, name: str, *args):
     """Call a stream-ordered entry point on the current stream of `dev`."""
+    index = dev.index
     fn = getattr(_lib or lib(), name)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if index == _get_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        status = fn(*args, _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream().cuda_stream)
-    if status != MILO_OK:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(index))
+    if status:
         _check(status, name)
 
 
@@ -561,10 +566,13 @@ def _slots(route: dict, what: str) -> tuple:
     """T, k and the inverse permutation of a route dict (milo_route's `ids`
     [T, k] and `inv_perm` [T*k])."""
     ids, inv = route["ids"], route["inv_perm"]
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError(f"{what}: route['ids'] must be [T, k]")
-    T, k = ids.shape
-    _arg(inv, "route['inv_perm']", (torch.int32,), min_numel=T * k)
+    T, k = shape
+    if not (isinstance(inv, torch.Tensor) and inv.dtype is torch.int32 and inv.numel() >= T * k and inv.is_cuda and
+            inv.is_contiguous()):
+        _arg(inv, "route['inv_perm']", (torch.int32,), min_numel=T * k)
     return T, k, inv
 
 
@@ -597,7 +605,8 @@ def milo_dispatch(x: torch.Tensor, route: dict, w: torch.Tensor | None = None, o
     _weights(w, T, k, dev)
     xs = _out(xs, "xs", (T * k, H), out_dtype or x.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dispatch", _p(x), _dt(x), T, k, H, _p(inv), _p(w), _p(xs), _dt(xs), _p(dev_status))
+    _launch(dev, "milo_dispatch", x.data_ptr(), _DT[x.dtype], T, k, H, inv.data_ptr(), _p(w), xs.data_ptr(),
+            _DT[xs.dtype], _p(dev_status))
     return xs
 
 
@@ -617,8 +626,8 @@ def milo_combine(ys: torch.Tensor, route: dict, w: torch.Tensor | None = None, r
     if residual is not None:
         _rows(residual, "residual", T, H, y.dtype, dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_combine", _p(ys), _dt(ys), T, k, H, _p(inv), _p(w), _p(residual), _p(y), _dt(y),
-            _p(dev_status))
+    _launch(dev, "milo_combine", ys.data_ptr(), _DT[ys.dtype], T, k, H, inv.data_ptr(), _p(w), _p(residual),
+            y.data_ptr(), _DT[y.dtype], _p(dev_status))
     return y
 
 
@@ -690,8 +699,10 @@ def _dense_args(x, W, act: str) -> tuple:
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M, {K}]")
     dev = x.device
-    _arg(x, "x", _ACT)
-    _need(W, "W", (x.dtype,), (N, K), dev)
+    if not (x.dtype in _ACT and x.is_cuda and x.is_contiguous()):
+        _arg(x, "x", _ACT)
+    if not (W.dtype is x.dtype and W.get_device() == dev.index and W.is_contiguous()):
+        _arg(W, "W", (x.dtype,), device=dev)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}, not {act!r}")
     return x.shape[0], N, K, dev, _ACTS[act]
@@ -716,8 +727,8 @@ def milo_dense_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | Non
     if z is not None:
         _need(z, "z", (x.dtype,), (M, N), dev)
     _status_arg(dev_status, dev)
-    _launch(dev, "milo_dense_linear", _p(x), _p(W), _dt(x), M, N, K, _p(bias), _p(residual), a, _p(y),
-            _dt(y), _p(z), _p(dev_status))
+    _launch(dev, "milo_dense_linear", x.data_ptr(), W.data_ptr(), _DT[x.dtype], M, N, K, _p(bias), _p(residual), a,
+            y.data_ptr(), _DT[y.dtype], _p(z), _p(dev_status))
     return y
 
 
