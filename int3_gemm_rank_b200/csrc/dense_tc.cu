@@ -28,6 +28,12 @@
 //     costs a tile of 16 columns, not of 128 rows.
 //   - Ragged edges need no care in the loads (TMA fills zeros) and are cut in
 //     the epilogue's stores.
+//   - Outputs of whole 16-byte pieces leave by TMA, and a residual's blocks come
+//     by it, up to three ahead of the accumulators (2780 x 8424 x 72 with both: 47
+//     us, 99 with loads that a warp waits for).  Other widths go through a staging
+//     buffer by words or elements, eight loads under way (2780 x 8420 x 72: 69 us,
+//     2780 x 8419 x 72: 96; one load at a time 268).  The two forms are kernels of
+//     their own: in one, the second's registers slowed the first by 3 to 15%.
 //   - Every wait is bounded: on a timeout the kernel flags MILO_DEV_TIMEOUT,
 //     waits for its copies and products and frees TMEM before it leaves.
 //
@@ -60,29 +66,28 @@ constexpr int kDtThreads = 32 * (2 + kDtEpiWarps);   // producer, MMA, epilogue
 constexpr int kDtMaxStages = 12;
 constexpr int kDtMaxSplit = 8;               // portable cluster size
 constexpr int kDtChunk = 32;                 // accumulator columns handled at a time
+constexpr int kDtOutBufs = 4;                // output buffers of an epilogue warp, at most
 constexpr int kDtBias = 128;                 // fp32 bias columns, per epilogue warp (its half of 256)
 
-// Output staging of an epilogue warp: 32 rows of 32 elements, 16 bytes apart
-// from a multiple of 128 so that 16-byte pieces of a column fall on different
-// banks.
+// Output staging of an epilogue warp (narrow form): 32 rows of 32 elements, 16
+// bytes apart from a multiple of 128 so that 16-byte pieces of a column fall on
+// different banks.
 constexpr int dense_pitch(int esize) { return 32 * esize + 16; }
 
 // One product of a launch.
 struct DenseProb {
     CUtensorMap a_map, b_map;
-    CUtensorMap y_map;                       // set when `store`
+    CUtensorMap y_map;                       // wide form only
     int P, Q, C;
     int a_mn, b_mn;
     int kblocks;                             // slices of 64 c
     int tiles_p, tiles_q, tiles;
     uint32_t idesc;
-    int vec;                                 // 16-byte output rows
-    int store;                               // ... and no residual: blocks of y (and z) leave by TMA
     void* y;                                 // [P, Q] (SWAP: [Q, P])
 };
 
 struct DenseTc {
-    CUtensorMap z_map;
+    CUtensorMap z_map, r_map;                // wide form only
     DenseProb prob[2];                       // one product, or two that share the grid (a layer's dx and dW)
     int tiles;                               // of both
     int bf16, bn, stages, split;             // columns of a tile; CTAs that share a tile's c
@@ -90,7 +95,7 @@ struct DenseTc {
     uint32_t tmem_cols;
     int bufs;                                // accumulators in TMEM (2: persistent)
     int stage_bytes, staging, off_staging, off_bias, off_bar;
-    int out_bufs, out_bytes;                 // TMA store: buffers of an epilogue warp, bytes of one
+    int out_bufs, out_bytes;                 // wide form: output buffers of an epilogue warp, bytes of one
     // epilogue (residual and z as y; SWAP: p is the feature)
     const void *bias, *residual;
     void* z;
@@ -189,57 +194,145 @@ __device__ __forceinline__ DenseItem dense_tile(const DenseTc& p, int item) {
 }
 
 // ---------------------------------------------------------------------------
-// epilogue of 32 rows (lane = row p) by 32 columns q0.. of D, normal form:
-// y[p, q].  v holds the lane's row.  st32 is the warp's staging buffer.
+// epilogue of 32 rows (lane = row p) by 32 columns q0.. of D, row form: y[p, q].
+// v holds the lane's row.  Wide form: rows of whole 16-byte pieces at 16-byte
+// addresses, blocks come and go by TMA, which cuts what lies outside.  Narrow
+// form: every other width and address.
 // ---------------------------------------------------------------------------
 
-// The warp's 32 x 32 block between staging rows and global rows p0.., columns
-// q0..; 16-byte pieces when d.vec.
-template <int DT, bool LOAD>
-__device__ __forceinline__ void dense_block(const DenseTc& p, const DenseProb& d, void* g, uint8_t* stg, int p0, int q0, int lane) {
-    constexpr int E = DT == MILO_F32 ? 4 : 2, kPitch = dense_pitch(E);
-    constexpr int kPieces = 32 * E / 16;              // 16-byte pieces of a row
-    constexpr int kRows = 32 / kPieces;               // rows of one pass
-    if (d.vec) {
-        const int piece = lane % kPieces, r0 = lane / kPieces;
-        const bool in = q0 + piece * (16 / E) < d.Q;  // Q is a multiple of a piece here
-        uint8_t* gp = static_cast<uint8_t*>(g) + (static_cast<size_t>(p0 + r0) * d.Q + q0) * E + piece * 16;
-        uint4 t[32 / kRows];
+// 16-byte piece i of the lane's row in a buffer of the maps' swizzled layout
+// (64-byte rows: piece i at i ^ ((row / 2) % 4); 128-byte rows: i ^ (row % 8), so
+// that eight lanes' pieces fall on different banks).
+template <int DT>
+__device__ __forceinline__ uint4* out_piece(uint8_t* buf, int lane, int i) {
+    if constexpr (DT == MILO_F32) return reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4));
+    else return reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+}
+
+template <int DT>
+__device__ __forceinline__ void wide_put(const CUtensorMap* map, const float (&v)[32], uint8_t* buf, int p0, int q0, int lane,
+                                         int32_t& st) {
+    if constexpr (DT == MILO_F32) {
 #pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
-            if constexpr (LOAD) {
-                if (in && p0 + r0 + i * kRows < d.P) t[i] = *reinterpret_cast<const uint4*>(gp + static_cast<size_t>(i) * kRows * d.Q * E);
-            } else {
-                t[i] = *reinterpret_cast<const uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
-            if constexpr (LOAD) {
-                *reinterpret_cast<uint4*>(stg + (r0 + i * kRows) * kPitch + piece * 16) = t[i];
-            } else {
-                if (in && p0 + r0 + i * kRows < d.P) *reinterpret_cast<uint4*>(gp + static_cast<size_t>(i) * kRows * d.Q * E) = t[i];
-            }
-        }
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(out_piece<DT>(buf, lane, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
-        using T = typename std::conditional<E == 4, uint32_t, uint16_t>::type;
-        if (q0 + lane < d.Q) {
-            T* gp = static_cast<T*>(g) + static_cast<size_t>(p0) * d.Q + q0 + lane;
-            T* sp = reinterpret_cast<T*>(stg) + lane;
-            const int n = min(32, d.P - p0);
-#pragma unroll 8
-            for (int r = 0; r < n; ++r) {
-                if constexpr (LOAD) sp[r * (kPitch / E)] = gp[static_cast<size_t>(r) * d.Q];
-                else gp[static_cast<size_t>(r) * d.Q] = sp[r * (kPitch / E)];
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack16<DT>(v[2 * i], v[2 * i + 1]);
+        if constexpr (DT == MILO_F16) half_range(v, w, st);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *out_piece<DT>(buf, lane, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+            "cp.async.bulk.commit_group;"
+            ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(buf)), "r"(q0), "r"(p0) : "memory");
+}
+
+// All but the `newest` last stores of this thread have left shared memory.
+__device__ __forceinline__ void stores_read(int newest) {
+    if (newest >= 3) asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+    else if (newest == 2) asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");
+    else if (newest == 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void add_bias(float (&v)[32], const float* bias) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 t = reinterpret_cast<const float4*>(bias)[i];
+        v[4 * i] += t.x;
+        v[4 * i + 1] += t.y;
+        v[4 * i + 2] += t.z;
+        v[4 * i + 3] += t.w;
+    }
+}
+
+// One 32 x 32 block.  `buf` holds the residual's block if there is one; the
+// stores up to the `left` newest have to be out of `zbuf`, and without a residual
+// out of `buf`, before they are written.
+__device__ __forceinline__ void wide_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* buf, uint8_t* zbuf,
+                                           int left, const float* bias, int p0, int q0, int lane, int32_t& st) {
+    if (p.bias) add_bias(v, bias);
+    if (p.z) {
+        if (lane == 0) stores_read(left);
+        __syncwarp();
+        if (p.bf16) wide_put<MILO_BF16>(&p.z_map, v, zbuf, p0, q0, lane, st);
+        else wide_put<MILO_F16>(&p.z_map, v, zbuf, p0, q0, lane, st);
+    }
+    act_tile(p.act, v);
+    with_dtype(p.y_dt, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < (DT == MILO_F32 ? 8 : 4); ++i) {
+                const uint4 t = *out_piece<DT>(buf, lane, i);
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+                if constexpr (DT == MILO_F32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[4 * i + q] += __uint_as_float(w[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[8 * i + q] += unpack16<DT>(w[q / 2], q & 1);
+                }
             }
+        } else {
+            if (lane == 0) stores_read(left);
+            __syncwarp();
+        }
+        wide_put<DT>(&d.y_map, v, buf, p0, q0, lane, st);
+    });
+}
+
+// Narrow form: the warp's block between staging rows (dense_pitch) and global
+// rows p0.., columns q0.., in pieces of T, R rows a pass.  All of a batch's
+// loads come before its stores: one at a time they would wait for each other
+// (the compiler cannot tell the two buffers apart).
+template <typename T, int E, bool LOAD>
+__device__ __forceinline__ void narrow_block_by(const DenseProb& d, void* g, uint8_t* stg, int p0, int q0, int lane) {
+    constexpr int kPitch = dense_pitch(E), kEl = static_cast<int>(sizeof(T)) / E;
+    constexpr int kLanes = 32 / kEl, R = 32 / kLanes, kBatch = 8;
+    const int col = lane % kLanes * kEl, r0 = lane / kLanes;
+    const int rows = q0 + col < d.Q ? d.P - p0 - r0 : 0;  // (Q is a multiple of kEl)
+    const size_t pitch = static_cast<size_t>(d.Q) * E;
+    uint8_t* gp = static_cast<uint8_t*>(g) + static_cast<size_t>(p0 + r0) * pitch + static_cast<size_t>(q0 + col) * E;
+    uint8_t* sp = stg + r0 * kPitch + col * E;
+#pragma unroll 1
+    for (int r = 0; r < 32; r += kBatch * R, gp += kBatch * R * pitch, sp += kBatch * R * kPitch) {
+        T t[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if constexpr (LOAD) t[i] = r + i * R < rows ? *reinterpret_cast<const T*>(gp + i * R * pitch) : T(0);
+            else t[i] = *reinterpret_cast<const T*>(sp + i * R * kPitch);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if constexpr (LOAD) *reinterpret_cast<T*>(sp + i * R * kPitch) = t[i];
+            else if (r + i * R < rows) *reinterpret_cast<T*>(gp + i * R * pitch) = t[i];
         }
     }
 }
 
-// The lane's 32 values to its staging row, and the block to global memory.
+template <int DT, bool LOAD>
+__device__ __forceinline__ void narrow_block(const DenseProb& d, const void* g, uint8_t* stg, int p0, int q0, int lane) {
+    if constexpr (DT == MILO_F32) {
+        narrow_block_by<uint32_t, 4, LOAD>(d, const_cast<void*>(g), stg, p0, q0, lane);
+    } else {
+        // words where every row starts on one, else elements
+        if (((reinterpret_cast<uintptr_t>(g) & 3) | (d.Q & 1)) == 0)
+            narrow_block_by<uint32_t, 2, LOAD>(d, const_cast<void*>(g), stg, p0, q0, lane);
+        else
+            narrow_block_by<uint16_t, 2, LOAD>(d, const_cast<void*>(g), stg, p0, q0, lane);
+    }
+}
+
 template <int DT>
-__device__ __forceinline__ void dense_put(const DenseTc& p, const DenseProb& d, void* g, const float (&v)[32], uint8_t* stg, int p0, int q0,
-                                          int lane, int32_t& st) {
+__device__ __forceinline__ void narrow_put(const DenseProb& d, void* g, const float (&v)[32], uint8_t* stg, int p0, int q0,
+                                           int lane, int32_t& st) {
     uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
     if constexpr (DT == MILO_F32) {
 #pragma unroll
@@ -255,109 +348,39 @@ __device__ __forceinline__ void dense_put(const DenseTc& p, const DenseProb& d, 
             reinterpret_cast<uint4*>(row)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
     __syncwarp();
-    dense_block<DT, false>(p, d, g, stg, p0, q0, lane);
+    narrow_block<DT, false>(d, g, stg, p0, q0, lane);
     __syncwarp();
 }
 
-// v += the block of the residual.
-template <int DT>
-__device__ __forceinline__ void dense_add(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg, int p0, int q0, int lane) {
-    dense_block<DT, true>(p, d, const_cast<void*>(p.residual), stg, p0, q0, lane);
-    __syncwarp();
-    const uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
-    if constexpr (DT == MILO_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 t = reinterpret_cast<const float4*>(row)[i];
-            v[4 * i] += t.x;
-            v[4 * i + 1] += t.y;
-            v[4 * i + 2] += t.z;
-            v[4 * i + 3] += t.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 t = reinterpret_cast<const uint4*>(row)[i];
-            const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[8 * i + q] += unpack16<DT>(w[q / 2], q & 1);
-        }
+__device__ __forceinline__ void narrow_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg,
+                                             const float* bias, int p0, int q0, int lane, int32_t& st) {
+    if (p.bias) add_bias(v, bias);
+    if (p.z) {
+        if (p.bf16) narrow_put<MILO_BF16>(d, p.z, v, stg, p0, q0, lane, st);
+        else narrow_put<MILO_F16>(d, p.z, v, stg, p0, q0, lane, st);
     }
-    __syncwarp();
-}
-
-// Which of the warp's TMA store buffers comes next.
-struct DenseOut {
-    uint8_t* stg;
-    int next;
-};
-
-// The warp's 32 x 32 block to rows p0.., columns q0.. by a TMA store, which cuts
-// what lies outside: the lane's row into a buffer in the map's swizzled layout
-// (64-byte rows: 16-byte piece c at c ^ ((row / 2) % 4); 128-byte rows: c ^ (row
-// % 8), so that eight lanes' pieces fall on different banks), one copy out.
-template <int DT>
-__device__ __forceinline__ void dense_tma_put(const DenseTc& p, const CUtensorMap* map, const float (&v)[32], DenseOut& o,
-                                              int p0, int q0, int lane, int32_t& st) {
-    if (lane == 0) {
-        // the buffer's last copy has read it
-        if (p.out_bufs == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    }
-    __syncwarp();
-    uint8_t* buf = o.stg + o.next * p.out_bytes;
-    if constexpr (DT == MILO_F32) {
-        uint8_t* row = buf + lane * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack16<DT>(v[2 * i], v[2 * i + 1]);
-        if constexpr (DT == MILO_F16) half_range(v, w, st);
-        uint8_t* row = buf + lane * 64;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(row + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
-            "cp.async.bulk.commit_group;"
-            ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(buf)), "r"(q0), "r"(p0) : "memory");
-    if (p.out_bufs == 2) o.next ^= 1;
-}
-
-__device__ __forceinline__ void dense_store_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], DenseOut& o,
-                                                  const float* bias, int p0, int q0, int lane, int32_t& st) {
-    if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 t = reinterpret_cast<const float4*>(bias)[i];
-            v[4 * i] += t.x;
-            v[4 * i + 1] += t.y;
-            v[4 * i + 2] += t.z;
-            v[4 * i + 3] += t.w;
-        }
-    }
-    if (p.z)
-        with_dtype(p.bf16 ? MILO_BF16 : MILO_F16, [&](auto dt) {
-            constexpr int DT = decltype(dt)::value;
-            if (d.store) dense_tma_put<DT>(p, &p.z_map, v, o, p0, q0, lane, st);
-            else dense_put<DT>(p, d, p.z, v, o.stg, p0, q0, lane, st);
-        });
     act_tile(p.act, v);
     with_dtype(p.y_dt, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (d.store) {
-            dense_tma_put<DT>(p, &d.y_map, v, o, p0, q0, lane, st);
-        } else {
-            if (p.residual) dense_add<DT>(p, d, v, o.stg, p0, q0, lane);
-            dense_put<DT>(p, d, d.y, v, o.stg, p0, q0, lane, st);
+        if (p.residual) {
+            narrow_block<DT, true>(d, p.residual, stg, p0, q0, lane);
+            __syncwarp();
+            const uint8_t* row = stg + lane * dense_pitch(DT == MILO_F32 ? 4 : 2);
+#pragma unroll
+            for (int i = 0; i < (DT == MILO_F32 ? 8 : 4); ++i) {
+                const uint4 t = reinterpret_cast<const uint4*>(row)[i];
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+                if constexpr (DT == MILO_F32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[4 * i + q] += __uint_as_float(w[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[8 * i + q] += unpack16<DT>(w[q / 2], q & 1);
+                }
+            }
+            __syncwarp();
         }
+        narrow_put<DT>(d, d.y, v, stg, p0, q0, lane, st);
     });
 }
 
@@ -397,7 +420,7 @@ __device__ __forceinline__ void dense_store_swapped(const DenseTc& p, const Dens
     });
 }
 
-template <bool SWAP, bool TWO>
+template <bool SWAP, bool TWO, bool WIDE>
 __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_constant__ DenseTc p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -406,7 +429,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     uint64_t* afull = empty + kDtMaxStages;      // accumulator finished
     uint64_t* aempty = afull + 2;                // accumulator read
     uint64_t* done_bar = aempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+    uint64_t* rbar = done_bar + 1;               // residual blocks, per epilogue warp and buffer
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + kDtEpiWarps * kDtOutBufs);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t cta = TWO || p.split > 1 ? cluster_rank() : 0u;
     const uint32_t rank = TWO ? 0u : cta;        // of a split of c
@@ -430,6 +454,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 mbar_init(&aempty[b], TWO ? 2 * kDtEpiWarps : kDtEpiWarps);
             }
             mbar_init(done_bar, 1);
+            if (WIDE && p.residual)
+                for (int i = 0; i < kDtEpiWarps * kDtOutBufs; ++i) mbar_init(&rbar[i], 1);
             fence_barrier_init();
         }
         __syncwarp();
@@ -467,7 +493,14 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     // epilogue warps: lane quarter, which half of the column blocks, own buffers
     const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
-    DenseOut out{smem + p.off_staging + ew * p.staging, 0};
+    uint8_t* stg = smem + p.off_staging + ew * p.staging;
+    // z's buffer, wide form: the one behind the others when those hold residuals
+    uint8_t* zbuf = stg + p.out_bufs * p.out_bytes;
+    auto load_residual = [&](int buf, int p0, int q0) {       // one lane
+        uint64_t* bar = &rbar[ew * kDtOutBufs + buf];
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.out_bytes));
+        tma_load_2d(stg + buf * p.out_bytes, &p.r_map, bar, q0, p0);
+    };
     float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + ew * kDtBias;
 
     if (warp == 0) {
@@ -574,6 +607,31 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         // ---------------------------------------------------------------- epilogue, whole tiles
         int buf = 0;
         uint32_t bph = 0;
+        bool dead = false;
+        // Wide form: the output buffers in turn; with a residual, its block comes
+        // to the buffer of y's, under way out_bufs - 1 blocks ahead.
+        int at = 0, flying = 0, ahead_it = first, ahead_c = -2 * W + W * half;
+        uint32_t rph = 0;
+        const bool res = WIDE && p.residual;
+        auto ahead = [&](int b) {                             // the next block's residual to buffer b
+            while (!dead) {
+                ahead_c += 2 * W;
+                if (ahead_c >= p.bn) {
+                    ahead_c = W * half;
+                    ahead_it += step;
+                }
+                if (ahead_it >= p.tiles) return;
+                const DenseItem t = dense_tile(p, ahead_it);
+                const DenseProb& d = p.prob[t.i];
+                const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0) + 32 * quarter, q0 = t.tq * p.bn + ahead_c;
+                if (p0 >= d.P || q0 >= d.Q || ahead_c >= p.bn) continue;
+                if (lane == 0) load_residual(b, p0, q0);
+                ++flying;
+                return;
+            }
+        };
+        if (res)
+            for (int b = 0; b < p.out_bufs - 1; ++b) ahead(b);
         for (int it = first; it < p.tiles; it += step) {
             const DenseItem t = dense_tile(p, it);
             const DenseProb& d = p.prob[t.i];
@@ -588,10 +646,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                     __syncwarp();
                 }
             }
-            if (!warp_wait(&afull[buf], bph)) {
-                st_bits |= MILO_DEV_TIMEOUT;
-                break;
-            }
+            // after a timeout nothing is waited for again (the outputs are invalid)
+            if (!dead && !warp_wait(&afull[buf], bph)) dead = true;
             tc_fence_after();
             const uint32_t acc = lane_base + static_cast<uint32_t>(buf * p.bn);
             for (int c = W * half; c < p.bn; c += 2 * W) {
@@ -602,8 +658,31 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
                 if (p0 >= d.P || q0 + c >= d.Q) continue;
-                if constexpr (SWAP) dense_store_swapped(p, d, v, p0, q0 + c, lane, st_bits);
-                else dense_store_chunk(p, d, v, out, sbias + c / 2 - W / 2 * half, p0, q0 + c, lane, st_bits);
+                const float* cb = sbias + c / 2 - W / 2 * half;
+                if constexpr (SWAP) {
+                    dense_store_swapped(p, d, v, p0, q0 + c, lane, st_bits);
+                } else if constexpr (WIDE) {
+                    if (res) {
+                        if (flying > 0) {
+                            --flying;
+                            if (!warp_wait(&rbar[ew * kDtOutBufs + at], rph)) dead = true;
+                        }
+                        wide_chunk(p, d, v, stg + at * p.out_bytes, zbuf, 1, cb, p0, q0 + c, lane, st_bits);
+                        // the buffer of the block before takes the next residual
+                        if (lane == 0) stores_read(1);
+                        __syncwarp();
+                        ahead(at == 0 ? p.out_bufs - 1 : at - 1);
+                        if (++at == p.out_bufs) { at = 0; rph ^= 1; }
+                    } else {
+                        uint8_t* zb = stg + at * p.out_bytes;
+                        if (p.z && ++at == p.out_bufs) at = 0;
+                        uint8_t* yb = stg + at * p.out_bytes;
+                        if (++at == p.out_bufs) at = 0;
+                        wide_chunk(p, d, v, yb, zb, p.out_bufs - 1, cb, p0, q0 + c, lane, st_bits);
+                    }
+                } else {
+                    narrow_chunk(p, d, v, stg, cb, p0, q0 + c, lane, st_bits);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -613,6 +692,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
             }
             if (++buf == p.bufs) { buf = 0; bph ^= 1; }
         }
+        if (dead) st_bits |= MILO_DEV_TIMEOUT;
     } else {
         // ---------------------------------------------------------------- epilogue, split over the cluster:
         // this CTA's partial blocks to their owners: block u (rows 32 (u % 4)..,
@@ -620,6 +700,13 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         // columns of a lane's row together
         const DenseProb& d = p.prob[dense_tile(p, first).i];
         const bool none = slice(d, rank) == slice(d, rank + 1);      // a short c leaves some CTAs nothing
+        if (WIDE && p.residual && lane == 0) {
+            // the residual of the first block this warp will finish
+            const DenseItem t = dense_tile(p, first);
+            const int u = ew * p.split + static_cast<int>(rank);
+            const int p0 = t.tp * kDtRows + 32 * (u & 3), q0 = t.tq * p.bn + W * (u >> 2);
+            if (u < 4 * (p.bn / W) && p0 < d.P && q0 < d.Q) load_residual(0, p0, q0);
+        }
         if (!warp_wait(&afull[0], 0)) st_bits |= MILO_DEV_TIMEOUT;
         tc_fence_after();
         __syncwarp();
@@ -660,6 +747,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         if (warp >= 2) {
             const DenseItem t = dense_tile(p, first);
             const DenseProb& d = p.prob[t.i];
+            uint32_t uph = 0;
             for (int i = ew; i * p.split + static_cast<int>(rank) < 4 * (p.bn / W); i += kDtEpiWarps) {
                 const int u = i * p.split + static_cast<int>(rank);
                 const int p0 = t.tp * kDtRows + 32 * (u & 3), q0 = t.tq * p.bn + W * (u >> 2);
@@ -684,13 +772,31 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                         sbias[lane] = q0 + lane < d.Q ? load16(p.bias, q0 + lane, p.bf16) : 0.0f;
                         __syncwarp();
                     }
-                    dense_store_chunk(p, d, v, out, sbias, p0, q0, lane, st_bits);
+                    if constexpr (WIDE) {
+                        if (p.residual) {
+                            // (the first block's is under way, the others' come now)
+                            if (i != ew && lane == 0) {
+                                stores_read(0);
+                                load_residual(0, p0, q0);
+                            }
+                            __syncwarp();
+                            if (!warp_wait(&rbar[ew * kDtOutBufs], uph)) st_bits |= MILO_DEV_TIMEOUT;
+                            uph ^= 1;
+                            wide_chunk(p, d, v, stg, zbuf, 1, sbias, p0, q0, lane, st_bits);
+                        } else {
+                            if (lane == 0) stores_read(0);
+                            __syncwarp();
+                            wide_chunk(p, d, v, zbuf - p.out_bytes, stg, p.out_bufs - 1, sbias, p0, q0, lane, st_bits);
+                        }
+                    } else {
+                        narrow_chunk(p, d, v, stg, sbias, p0, q0, lane, st_bits);
+                    }
                 }
             }
         }
     }
     // the stores have left shared memory and reached the outputs
-    if (!SWAP && warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (WIDE && warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     flag(p.dev_status, st_bits);
     tc_fence_before();
     __syncthreads();
@@ -721,23 +827,23 @@ static uint32_t dense_idesc(int bf16, int a_mn, int b_mn, int rows, int bn) {
            (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(rows >> 4) << 24);
 }
 
-template <bool SWAP, bool TWO>
+template <bool SWAP, bool TWO, bool WIDE>
 static cudaError_t dense_configure() {
     static std::atomic<bool> configured[64];     // set once per device (a repeat is harmless)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(dense_tc_kernel<SWAP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtSmemMax + 1024);
+        e = cudaFuncSetAttribute(dense_tc_kernel<SWAP, TWO, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDtSmemMax + 1024);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
     }
     return cudaSuccess;
 }
 
-template <bool SWAP, bool TWO>
+template <bool SWAP, bool TWO, bool WIDE>
 static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStream_t s) {
-    const cudaError_t e = dense_configure<SWAP, TWO>();
+    const cudaError_t e = dense_configure<SWAP, TWO, WIDE>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -753,7 +859,7 @@ static cudaError_t launch_dense_tc(const DenseTc& p, int grid, int smem, cudaStr
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = TWO || p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP, TWO>, p);
+    return cudaLaunchKernelEx(&cfg, dense_tc_kernel<SWAP, TWO, WIDE>, p);
 }
 
 // Clusters of `split` CTAs (with a whole SM's shared memory each) that run at
@@ -764,7 +870,7 @@ static int max_clusters(int split) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int n = known[dev][split].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    if (dense_configure<false, false>() != cudaSuccess) return 0;
+    if (dense_configure<false, false, true>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(split));
     cfg.blockDim = dim3(kDtThreads);
@@ -776,7 +882,7 @@ static int max_clusters(int split) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, dense_tc_kernel<false, false>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, dense_tc_kernel<false, false, true>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return 0;
     }
@@ -863,6 +969,7 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     DenseTc p;
     memset(&p, 0, sizeof(p));
     const void *a[2] = {}, *b[2] = {};
+    bool wide = !swap;
     long long lda[2] = {}, ldb[2] = {};
     for (int i = 0; i < n; ++i) {
         const DenseGemm& g = gs[i];
@@ -878,8 +985,6 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
         ldb[i] = swap ? g.lda : g.ldb;
         d.kblocks = (d.C + kDtK - 1) / kDtK;
         d.y = g.y;
-        d.vec = g.Q % 8 == 0 && aligned(g.y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
-        d.store = !swap && d.vec && !g.residual;
     }
     const DenseGemm& g = gs[0];
     const int sms = dense_sms();
@@ -921,23 +1026,29 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     p.stage_bytes = kDtAtom + b_rows * 128;
     // shared memory: the ring (then a split's partial blocks), the row form's
     // output buffers and bias, barriers
-    // (TMA stores from two buffers a warp where that costs the ring no stage of
-    // the four or more that keep it full)
     const int es = g.y_dt == MILO_F32 ? 4 : 2, bias = swap ? 0 : kDtEpiWarps * kDtBias * 4;
     const int want = std::max(2, p.bufs == 2 ? kDtMaxStages : kper);
-    bool store = !swap;
-    for (int i = 0; i < n; ++i) store = store && p.prob[i].store;
-    for (int i = 0; i < n; ++i) p.prob[i].store = store;
+    for (int i = 0; i < n; ++i)
+        wide = wide && p.prob[i].Q % 8 == 0 && aligned(p.prob[i].y, 16) && aligned(g.residual, 16) && aligned(g.z, 16);
+    const auto ring = [&](int staging) {
+        return std::min({kDtMaxStages, (kDtSmemMax - kDtEpiWarps * staging - bias - 1024) / p.stage_bytes, want});
+    };
     p.out_bytes = 32 * 32 * es;
-    auto ring = [&](int staging) { return std::min({kDtMaxStages, (kDtSmemMax - kDtEpiWarps * staging - bias - 512) / p.stage_bytes, want}); };
     p.out_bufs = 1;
-    p.staging = swap ? 0 : store ? p.out_bytes : 32 * dense_pitch(es);
-    p.stages = ring(p.staging);
-    if (store && ring(2 * p.out_bytes) >= std::min(p.stages, 4)) {
-        p.out_bufs = 2;
-        p.staging = 2 * p.out_bytes;
-        p.stages = ring(p.staging);
+    p.staging = swap ? 0 : 32 * dense_pitch(es);
+    if (wide) {
+        // Without a residual two buffers a warp let a store drain under the next
+        // block; with one they cover its latency (a split loads one block ahead
+        // and needs one).  As many as leave the ring four stages, or with a
+        // residual three, if it can have those at all.
+        const int z = g.residual && g.z ? 32 * 32 * 2 : 0;       // z's own, behind the others
+        const int least = g.residual && p.split == 1 ? 2 : 1, most = !g.residual ? 2 : p.split == 1 ? kDtOutBufs : 1;
+        const int enough = std::min(ring(least * p.out_bytes + z), g.residual ? 3 : 4);
+        p.out_bufs = most;
+        while (p.out_bufs > least && ring(p.out_bufs * p.out_bytes + z) < enough) --p.out_bufs;
+        p.staging = p.out_bufs * p.out_bytes + z;
     }
+    p.stages = ring(p.staging);
     const int staging = kDtEpiWarps * p.staging;
     const int w = swap ? 16 : kDtChunk;
     const int part = p.split > 1 ? static_cast<int>(round_up(4 * (p.bn / w), p.split)) * w * 128 : 0;
@@ -970,18 +1081,23 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
         st = d.b_mn ? make_map(&d.b_map, b[i], dt, d.Q, d.C, ldb[i] * 2, 64, kDtK, what, swz)
                     : make_map(&d.b_map, b[i], dt, d.C, d.Q, ldb[i] * 2, kDtK, b_rows, what, swz);
         if (st != MILO_OK) return st;
-        if (!d.store) continue;
+        if (!wide) continue;
         // output blocks of 32 x 32
-        st = make_map(&d.y_map, d.y, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt, d.Q, d.P, static_cast<uint64_t>(d.Q) * es,
-                      32, 32, what, es == 4 ? swz : CU_TENSOR_MAP_SWIZZLE_64B);
-        if (st == MILO_OK && i == 0 && p.z)
+        const CUtensorMapDataType ydt = es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt;
+        const CUtensorMapSwizzle yswz = es == 4 ? swz : CU_TENSOR_MAP_SWIZZLE_64B;
+        st = make_map(&d.y_map, d.y, ydt, d.Q, d.P, static_cast<uint64_t>(d.Q) * es, 32, 32, what, yswz);
+        if (st == MILO_OK && p.z)
             st = make_map(&p.z_map, p.z, dt, d.Q, d.P, static_cast<uint64_t>(d.Q) * 2, 32, 32, what, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (st == MILO_OK && p.residual)
+            st = make_map(&p.r_map, p.residual, ydt, d.Q, d.P, static_cast<uint64_t>(d.Q) * es, 32, 32, what, yswz);
         if (st != MILO_OK) return st;
     }
-    if (p.two) return check_cuda(launch_dense_tc<false, true>(p, 2 * std::min(p.tiles, slots), smem, s), what);
-    const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
-    return check_cuda(swap ? launch_dense_tc<true, false>(p, grid, smem, s) : launch_dense_tc<false, false>(p, grid, smem, s),
-                      what);
+    const int grid = p.two ? 2 * std::min(p.tiles, slots) : p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
+    cudaError_t e;
+    if (swap) e = launch_dense_tc<true, false, false>(p, grid, smem, s);
+    else if (p.two) e = wide ? launch_dense_tc<false, true, true>(p, grid, smem, s) : launch_dense_tc<false, true, false>(p, grid, smem, s);
+    else e = wide ? launch_dense_tc<false, false, true>(p, grid, smem, s) : launch_dense_tc<false, false, false>(p, grid, smem, s);
+    return check_cuda(e, what);
 }
 
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {

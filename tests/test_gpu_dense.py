@@ -169,6 +169,37 @@ def test_in_place_residual_views_and_an_empty_batch(milo):
     assert g["dx"].shape == (0, 128) and not g["dW"].any() and not g["db"].any()
 
 
+# a split sum, tiles of single CTAs, of pairs; each with rows of whole 16-byte
+# pieces, of whole words, of odd elements
+@pytest.mark.parametrize("M,N,K", [(300, 64, 2048), (300, 66, 2048), (301, 63, 2048), (20001, 120, 72), (20001, 122, 72),
+                                   (20001, 121, 72), (2600, 2312, 264), (2600, 2310, 264), (2601, 2311, 264)])
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_residuals_in_place_in_every_form(milo, M, N, K, dt, out):
+    rng = np.random.default_rng(M + N)
+    x, W, b = rand(rng, (M, K), dt), rand(rng, (N, K), dt, K ** -0.5), rand(rng, (N,), dt)
+    buf = rand(rng, (M + 40, N), out)            # rows behind the last stay as they are
+    tail, r = buf[M:].clone(), buf[:M].clone()
+    zt = torch.full((M + 40, N), 7.0, dtype=DT[dt], device="cuda")
+    yr, yb, zr, zb = R.linear(n64(x), n64(W), n64(b), "silu", n64(r), dt, out)
+    y = milo.milo_dense_linear(x, W, b, "silu", r, z=zt[:M])
+    check(y, yr, yb, "y")
+    check(zt[:M], zr, zb, "z")
+    milo.milo_dense_linear(x, W, b, "silu", buf[:M], y=buf[:M])
+    assert torch.equal(buf[:M], y) and torch.equal(buf[M:], tail) and bool((zt[M:] == 7.0).all())
+
+
+@pytest.mark.parametrize("M,N", [(65, 63), (300, 66), (300, 64), (2601, 2311), (2600, 2312)])
+def test_no_range_flag_from_outside_the_rows(milo, M, N):
+    """Pre-activations at fp16's largest value and a residual that takes them
+    back to zero: nothing is out of range, in no row or column of a ragged tile."""
+    x, W = torch.zeros((M, 64), dtype=torch.float16, device="cuda"), torch.zeros((N, 64), dtype=torch.float16, device="cuda")
+    b = torch.full((N,), 65504.0, dtype=torch.float16, device="cuda")
+    r = torch.full((M, N), -65504.0, dtype=torch.float16, device="cuda")
+    z, st = torch.empty_like(r), milo.new_status()
+    y = milo.milo_dense_linear(x, W, b, "none", r, z=z, dev_status=st)
+    assert not y.any() and bool((z == 65504.0).all()) and int(st.item()) == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 24, 131072), (20, 40, 65536), (300, 40, 16384), (700, 130, 520)])
 def test_long_sums_and_fp32_residuals(milo, M, N, K):
     rng = np.random.default_rng(K)
