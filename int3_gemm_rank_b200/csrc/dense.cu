@@ -150,11 +150,14 @@ static cudaError_t run_dz(const DzParams& p, bool vec, int grid, cudaStream_t s)
     return run_dz_vec<MILO_BF16, ZT>(p, vec, grid, s);
 }
 
-// db[n] = the row blocks' sums: eight lanes of a column take every eighth block
-// in order, and meet in lane order.
-__global__ void __launch_bounds__(256) dense_db_kernel(const float* __restrict__ part, int blocks, int N, int bf16,
-                                                       uint16_t* __restrict__ db, int32_t* dev_status) {
-    __shared__ float red[8][32];
+// db[n] = the row blocks' sums: LANES lanes of a column take every LANES'th block
+// in order, and meet in lane order.  Bound by the latency of its loads: 32 lanes
+// where there are many blocks (979 blocks of 78 columns, db in all 7.0 us, with
+// eight lanes 10.0; 96 blocks of 1411 columns 8.7 and 7.8).
+template <int LANES>
+__global__ void __launch_bounds__(32 * LANES) dense_db_kernel(const float* __restrict__ part, int blocks, int N, int bf16,
+                                                                 uint16_t* __restrict__ db, int32_t* dev_status) {
+    __shared__ float red[LANES][32];
     grid_dep_launch();
     grid_dep_wait();
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -162,13 +165,13 @@ __global__ void __launch_bounds__(256) dense_db_kernel(const float* __restrict__
     float s = 0.0f;
     if (n < N)
 #pragma unroll 8
-        for (int b = rl; b < blocks; b += 8) s += part[static_cast<size_t>(b) * N + n];
+        for (int b = rl; b < blocks; b += LANES) s += part[static_cast<size_t>(b) * N + n];
     red[rl][lane] = s;
     __syncthreads();
     if (rl > 0 || n >= N) return;
     int32_t st = 0;
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += red[q][lane];
+    for (int q = 1; q < LANES; ++q) s += red[q][lane];
     db[n] = round16(s, bf16, st);
     flag(dev_status, st);
 }
@@ -290,7 +293,8 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
         if (s != MILO_OK) return s;
     }
     if (db && w.blocks > 1) {
-        s = check_cuda(launch_pdl(dense_db_kernel, dim3((N + 31) / 32), dim3(256), 0, st,
+        const bool many = w.blocks >= 256;
+        s = check_cuda(launch_pdl(many ? dense_db_kernel<32> : dense_db_kernel<8>, dim3((N + 31) / 32), dim3(many ? 1024 : 256), 0, st,
                                   reinterpret_cast<const float*>(base + w.part), w.blocks, N, dt == MILO_BF16 ? 1 : 0,
                                   static_cast<uint16_t*>(db), dev_status),
                        "db");

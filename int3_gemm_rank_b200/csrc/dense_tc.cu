@@ -897,9 +897,15 @@ struct DensePlan {
 // Columns of a tile and split of c, by an estimate in SM cycles of a CTA's
 // work: a slice of c takes bn * 2 cycles of the tensor core or its bytes at 66
 // bytes a cycle (what one SM was seen to draw from L2: 0.385 us for the 48 KB
-// of a 256-column slice), whichever is longer; a wave of tiles takes its
-// slices, and the last one an epilogue; all of it at least the operands' bytes
-// at the measured copy rate (23 bytes a cycle and SM).
+// of a 256-column slice), whichever is longer; a tile takes its slices or, where
+// these are few and another tile follows, its epilogue (600 and 20 a column: 3
+// us for 256); the first CTA has the most of the first product's tiles, then its
+// share of the second's; and the last tile an epilogue.  All of it at least the
+// operands' bytes at the measured copy rate (23 bytes a cycle and SM).
+static double tile_cycles(double slices, double slice, int bn, double waves) {
+    return waves > 1.0 ? std::max(slices * slice, 600.0 + 20.0 * bn) : slices * slice;
+}
+
 static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePlan* plan) {
     double best = -1.0, dram = 0.0;
     int qmax = 0, kmax = 0;
@@ -917,20 +923,16 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePl
         if (!swap && bn > 64 && bn - 64 >= qmax) break;          // the tile would be part empty
         const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 66.0);
         for (int split = 1; split <= kDtMaxSplit && (split == 1 || kmax >= 2 * split); ++split) {
-            double tiles = 0.0, slices = 0.0, longest = 0.0;
-            for (int i = 0; i < n; ++i) {
-                const double t = std::ceil(P[i] / 128.0) * std::ceil(Q[i] / static_cast<double>(bn));
-                const double k = std::ceil(kblocks[i] / split);
-                tiles += t;
-                slices += t * k;
-                longest = std::max(longest, k);
-            }
+            const auto count = [&](int i) { return std::ceil(P[i] / 128.0) * std::ceil(Q[i] / static_cast<double>(bn)); };
+            const double tiles = count(0) + (n > 1 ? count(1) : 0.0);
             // clusters only where one wave holds them all
             if (split > 1 && tiles > max_clusters(split)) break;
             const double waves = split > 1 ? 1.0 : std::ceil(tiles / sms);
-            const double work = waves == 1.0 ? longest : std::max(longest, waves * slices / tiles);
+            const double w0 = split > 1 ? 1.0 : std::ceil(count(0) / sms);
+            const auto cycles = [&](int i) { return tile_cycles(std::ceil(kblocks[i] / split), slice, bn, waves); };
+            const double work = w0 * cycles(0) + (waves - w0) * cycles(n - 1);
             const double epilogue = 8.0 * bn * (split > 1 ? 1.0 / split : 1.0);
-            const double cost = std::max(dram, (work + 0.5 * waves) * slice) + epilogue +
+            const double cost = std::max(dram, work + 0.5 * waves * slice) + epilogue +
                                 (split > 1 ? 1500.0 + 100.0 * split : 0.0);
             if (best < 0.0 || cost < best) {
                 best = cost;
@@ -942,17 +944,12 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePl
         // pairs of CTAs: 256 x 256 tiles, each CTA bringing half of either operand
         // (32 KB a slice against the tensor cores' 512 cycles)
         const int pairs = max_clusters(2);
-        double tiles = 0.0, slices = 0.0, longest = 0.0;
-        for (int i = 0; i < n; ++i) {
-            const double t = std::ceil(P[i] / 256.0) * std::ceil(Q[i] / 256.0);
-            tiles += t;
-            slices += t * kblocks[i];
-            longest = std::max(longest, kblocks[i]);
-        }
+        const auto count = [&](int i) { return std::ceil(P[i] / 256.0) * std::ceil(Q[i] / 256.0); };
         if (pairs > 0) {
-            const double waves = std::ceil(tiles / pairs);
-            const double work = waves == 1.0 ? longest : std::max(longest, waves * slices / tiles);
-            const double cost = std::max(dram, (work + 0.5 * waves) * 512.0) + 8.0 * 256 + 500.0;
+            const double waves = std::ceil((count(0) + (n > 1 ? count(1) : 0.0)) / pairs), w0 = std::ceil(count(0) / pairs);
+            const auto cycles = [&](int i) { return tile_cycles(kblocks[i], 512.0, 256, waves); };
+            const double work = w0 * cycles(0) + (waves - w0) * cycles(n - 1);
+            const double cost = std::max(dram, work + 0.5 * waves * 512.0) + 8.0 * 256 + 500.0;
             if (cost < best) {
                 best = cost;
                 *plan = DensePlan{256, 1, 1};
@@ -1100,24 +1097,28 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     return check_cuda(e, what);
 }
 
+// Few rows of A (tokens): they become the columns.
+static bool few_rows(const DenseGemm& g) { return g.P <= 128 && !g.a_mn; }
+
 milo_status launch_dense_gemm(const DenseGemm& g, const char* what, cudaStream_t s) {
     if (g.P <= kDenseFewRows && !g.a_mn && !g.b_mn) return launch_dense_few(g, what, s);
-    // few rows of A (tokens): they become the columns
-    return launch_dense(&g, 1, g.P <= 128 && !g.a_mn, what, s);
+    return launch_dense(&g, 1, few_rows(g), what, s);
 }
 
 milo_status launch_dense_pair(const DenseGemm& g0, const DenseGemm& g1, const char* what, cudaStream_t s) {
     // the longer sums first: the shorter ones fill the last wave
     const DenseGemm gs[2] = {g0.C >= g1.C ? g0 : g1, g0.C >= g1.C ? g1 : g0};
     if (!g0.y && !g1.y) return MILO_OK;
-    // one launch unless the two want different tiles or splits by more than a
-    // second launch costs (about 4000 cycles)
+    // one launch unless the two want different forms, tiles or splits by more
+    // than a second launch costs (about 4000 cycles).  By the shapes alone: a
+    // gradient without the other has the same bits.
     DensePlan plan;
     const int sms = dense_sms();
-    const double apart = dense_plan(&g0, 1, false, sms, &plan) + dense_plan(&g1, 1, false, sms, &plan) + 4000.0;
+    const bool few0 = few_rows(g0), few1 = few_rows(g1);
+    const double apart = dense_plan(&g0, 1, few0, sms, &plan) + dense_plan(&g1, 1, few1, sms, &plan) + 4000.0;
     if (dense_plan(gs, 2, false, sms, &plan) <= apart) return launch_dense(gs, 2, false, what, s);
-    milo_status r = g0.y ? launch_dense(&g0, 1, false, what, s) : MILO_OK;
-    if (r == MILO_OK && g1.y) r = launch_dense(&g1, 1, false, what, s);
+    milo_status r = g0.y ? launch_dense(&g0, 1, few0, what, s) : MILO_OK;
+    if (r == MILO_OK && g1.y) r = launch_dense(&g1, 1, few1, what, s);
     return r;
 }
 

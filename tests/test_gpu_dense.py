@@ -85,6 +85,13 @@ def test_backward(milo, M, N, K, dt, dyt, act):
         assert torch.equal(milo.milo_dense_linear_backward(dy, x, W, act, z, need=(name,))[name], g[name]), name
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 9001, 520), (18, 6288, 1032), (100, 4100, 1096), (128, 8192, 264), (129, 8195, 264)])
+@pytest.mark.parametrize("dt,dyt,act", [("bf16", "bf16", "none"), ("f16", "f16", "gelu")])
+def test_backward_of_few_tokens_and_wide_layers(milo, M, N, K, dt, dyt, act):
+    """Shapes whose two gradients want tiles of different kinds."""
+    test_backward(milo, M, N, K, dt, dyt, act)
+
+
 # tiles of pairs of CTAs (256 x 256), more tiles than fit at once, ragged on every side
 LARGE = [(2600, 2312, 648), (1537, 5000, 264), (4100, 1032, 512)]
 
