@@ -412,8 +412,8 @@ MILO_API milo_status milo_route_backward(const uint16_t* logits, const int32_t* 
  *   y         [M, N] in y_dt (F16, BF16 or F32), rounded once from fp32
  *   z         NULL, or [M, N] in dt: the pre-activation, which
  *             milo_dense_linear_backward needs when there is an activation
- * x and W 16-byte aligned, the others aligned to their elements; y and z
- * overlap no input but residual.  M = 0 does nothing.
+ * x and W 16-byte aligned, the others aligned to their elements; y overlaps no
+ * other buffer but residual's, z none.  M = 0 does nothing.
  * Errors: INVALID_ARG (M < 0, N or K < 1, unknown dtype or act, NULL or
  * misaligned pointers), UNSUPPORTED_SHAPE (K % 8, sizes above the limits),
  * CUDA.  Device: FP16_RANGE (an fp16 y or z overflows), TIMEOUT.  dev_status
