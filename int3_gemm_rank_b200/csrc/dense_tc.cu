@@ -17,7 +17,8 @@
 //     brings 128 rows of A and of B, 32 KB a slice instead of 48, since what
 //     an SM can draw from L2 (about 66 bytes a cycle) bounds the single form.
 //   - Two products may share a launch (a layer's dx and dW): their tiles follow
-//     one another on the same grid, so neither's last wave leaves SMs idle.
+//     one another on the same grid (dense_item), so neither's last wave leaves
+//     SMs idle.
 //   - Few tiles: c is split over the CTAs of a cluster.  The tile's blocks of
 //     32 rows by 32 (SWAP: 16) columns are dealt out to the CTAs; each sends its
 //     partial blocks to their owners' shared memory, and after a cluster
@@ -90,6 +91,7 @@ struct DenseTc {
     CUtensorMap z_map, r_map;                // wide form only
     DenseProb prob[2];                       // one product, or two that share the grid (a layer's dx and dW)
     int tiles;                               // of both
+    int rounds, extra, fill;                 // the schedule (dense_item)
     int bf16, bn, stages, split;             // columns of a tile; CTAs that share a tile's c
     int two;                                 // pairs of CTAs on tiles of 256 rows
     uint32_t tmem_cols;
@@ -180,6 +182,22 @@ struct DenseItem {
     int i;                                   // product
     int tp, tq;
 };
+// Item n of CTA (or pair, or cluster) `slot` of S, or -1 behind its last one; item
+// 0 is tile `slot`.
+// The first product's tiles, which take the longest, go round: `rounds` to
+// each slot and one more to the first `extra`.  The other slots then take
+// `fill` of the second's, about as long as that one, and the rest goes round
+// again.
+__device__ __forceinline__ int dense_item(const DenseTc& p, int slot, int S, int n) {
+    const int own = p.rounds + (slot < p.extra ? 1 : 0);
+    if (n < own) return n * S + slot;
+    const int m = n - own, others = S - p.extra;
+    int i = p.prob[0].tiles;
+    if (slot < p.extra) i += p.fill * others + m * S + slot;
+    else if (m < p.fill) i += m * others + slot - p.extra;
+    else i += p.fill * others + (m - p.fill) * S + slot;
+    return i < p.tiles ? i : -1;
+}
 __device__ __forceinline__ DenseItem dense_tile(const DenseTc& p, int item) {
     DenseItem r;
     r.i = item >= p.prob[0].tiles;
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     const auto slice = [&](const DenseProb& d, uint32_t r) {
         return static_cast<int>(static_cast<long long>(d.kblocks) * r / p.split);
     };
-    const int first = static_cast<int>(blockIdx.x) / group, step = static_cast<int>(gridDim.x) / group;
+    const int first = static_cast<int>(blockIdx.x) / group, slots = static_cast<int>(gridDim.x) / group;
     int32_t st_bits = 0;
     // epilogue warps: lane quarter, which half of the column blocks, own buffers
     const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         bool fail = false;
         const uint32_t tx = (TWO ? 2 : 1) * p.stage_bytes;
         const int bq = TWO ? p.bn / 2 : p.bn;        // B rows this CTA brings
-        for (int it = first; it < p.tiles && !fail; it += step) {
+        for (int n = 0, it = first; it >= 0 && !fail; it = dense_item(p, first, slots, ++n)) {
             const DenseItem t = dense_tile(p, it);
             const DenseProb& d = p.prob[t.i];
             const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0), q0 = t.tq * p.bn + (TWO ? bq * cta : 0);
@@ -559,7 +577,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         int stage = 0, buf = 0;
         uint32_t phase = 0, bph = 0;
         bool fail = false;
-        for (int it = first; it < p.tiles && !fail && (!TWO || cta == 0); it += step) {
+        for (int n = 0, it = first; it >= 0 && !fail && (!TWO || cta == 0); it = dense_item(p, first, slots, ++n)) {
             if (!warp_wait(&aempty[buf], bph ^ 1)) {
                 fail = true;
                 break;
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         bool dead = false;
         // Wide form: the output buffers in turn; with a residual, its block comes
         // to the buffer of y's, under way out_bufs - 1 blocks ahead.
-        int at = 0, flying = 0, ahead_it = first, ahead_c = -2 * W + W * half;
+        int at = 0, flying = 0, ahead_n = 0, ahead_it = first, ahead_c = -2 * W + W * half;
         uint32_t rph = 0;
         const bool res = WIDE && p.residual;
         auto ahead = [&](int b) {                             // the next block's residual to buffer b
@@ -618,9 +636,9 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 ahead_c += 2 * W;
                 if (ahead_c >= p.bn) {
                     ahead_c = W * half;
-                    ahead_it += step;
+                    if (ahead_it >= 0) ahead_it = dense_item(p, first, slots, ++ahead_n);
                 }
-                if (ahead_it >= p.tiles) return;
+                if (ahead_it < 0) return;
                 const DenseItem t = dense_tile(p, ahead_it);
                 const DenseProb& d = p.prob[t.i];
                 const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0) + 32 * quarter, q0 = t.tq * p.bn + ahead_c;
@@ -632,7 +650,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         };
         if (res)
             for (int b = 0; b < p.out_bufs - 1; ++b) ahead(b);
-        for (int it = first; it < p.tiles; it += step) {
+        for (int n = 0, it = first; it >= 0; it = dense_item(p, first, slots, ++n)) {
             const DenseItem t = dense_tile(p, it);
             const DenseProb& d = p.prob[t.i];
             const int p0 = t.tp * kTileRows2 + (TWO ? kDtRows * cta : 0) + 32 * quarter, q0 = t.tq * p.bn;
@@ -899,11 +917,22 @@ struct DensePlan {
 // bytes a cycle (what one SM was seen to draw from L2: 0.385 us for the 48 KB
 // of a 256-column slice), whichever is longer; a tile takes its slices or, where
 // these are few and another tile follows, its epilogue (600 and 20 a column: 3
-// us for 256); the first CTA has the most of the first product's tiles, then its
-// share of the second's; and the last tile an epilogue.  All of it at least the
-// operands' bytes at the measured copy rate (23 bytes a cycle and SM).
+// us for 256); and the last tile an epilogue.  All of it at least the operands'
+// bytes at the measured copy rate (23 bytes a cycle and SM).
 static double tile_cycles(double slices, double slice, int bn, double waves) {
     return waves > 1.0 ? std::max(slices * slice, 600.0 + 20.0 * bn) : slices * slice;
+}
+static double slice_cycles(int bn, int two) { return two ? 512.0 : std::max(2.0 * bn, (kDtAtom + bn * 128) / 66.0); }
+
+// Tiles of the second product for a slot without an extra one of the first's.
+static double fill_tiles(double c0, double c1) { return std::max(1.0, std::floor(c0 / c1)); }
+
+// The longest slot of dense_item's schedule: t0 tiles of c0 cycles, t1 of c1.
+static double schedule_cycles(double t0, double c0, double t1, double c1, double slots) {
+    const double rounds = std::floor(t0 / slots), extra = t0 - rounds * slots, others = slots - extra;
+    const double filled = std::min(t1, fill_tiles(c0, c1) * others);
+    return rounds * c0 + std::max(extra > 0.0 ? c0 : 0.0, std::ceil(filled / others) * c1) +
+           std::ceil((t1 - filled) / slots) * c1;
 }
 
 static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePlan* plan) {
@@ -921,16 +950,16 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePl
     const int bn_swap = static_cast<int>(round_up(qmax, 16));
     for (int bn = swap ? bn_swap : 64; bn <= (swap ? bn_swap : 256); bn += 64) {
         if (!swap && bn > 64 && bn - 64 >= qmax) break;          // the tile would be part empty
-        const double slice = std::max(2.0 * bn, (kDtAtom + bn * 128) / 66.0);
+        const double slice = slice_cycles(bn, 0);
         for (int split = 1; split <= kDtMaxSplit && (split == 1 || kmax >= 2 * split); ++split) {
             const auto count = [&](int i) { return std::ceil(P[i] / 128.0) * std::ceil(Q[i] / static_cast<double>(bn)); };
             const double tiles = count(0) + (n > 1 ? count(1) : 0.0);
             // clusters only where one wave holds them all
             if (split > 1 && tiles > max_clusters(split)) break;
             const double waves = split > 1 ? 1.0 : std::ceil(tiles / sms);
-            const double w0 = split > 1 ? 1.0 : std::ceil(count(0) / sms);
             const auto cycles = [&](int i) { return tile_cycles(std::ceil(kblocks[i] / split), slice, bn, waves); };
-            const double work = w0 * cycles(0) + (waves - w0) * cycles(n - 1);
+            const double work = split > 1 ? cycles(0)
+                                          : schedule_cycles(count(0), cycles(0), n > 1 ? count(1) : 0.0, cycles(n - 1), sms);
             const double epilogue = 8.0 * bn * (split > 1 ? 1.0 / split : 1.0);
             const double cost = std::max(dram, work + 0.5 * waves * slice) + epilogue +
                                 (split > 1 ? 1500.0 + 100.0 * split : 0.0);
@@ -946,9 +975,9 @@ static double dense_plan(const DenseGemm* gs, int n, bool swap, int sms, DensePl
         const int pairs = max_clusters(2);
         const auto count = [&](int i) { return std::ceil(P[i] / 256.0) * std::ceil(Q[i] / 256.0); };
         if (pairs > 0) {
-            const double waves = std::ceil((count(0) + (n > 1 ? count(1) : 0.0)) / pairs), w0 = std::ceil(count(0) / pairs);
-            const auto cycles = [&](int i) { return tile_cycles(kblocks[i], 512.0, 256, waves); };
-            const double work = w0 * cycles(0) + (waves - w0) * cycles(n - 1);
+            const double waves = std::ceil((count(0) + (n > 1 ? count(1) : 0.0)) / pairs);
+            const auto cycles = [&](int i) { return tile_cycles(kblocks[i], slice_cycles(256, 1), 256, waves); };
+            const double work = schedule_cycles(count(0), cycles(0), n > 1 ? count(1) : 0.0, cycles(n - 1), pairs);
             const double cost = std::max(dram, work + 0.5 * waves * 512.0) + 8.0 * 256 + 500.0;
             if (cost < best) {
                 best = cost;
@@ -1089,7 +1118,13 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
             st = make_map(&p.r_map, p.residual, ydt, d.Q, d.P, static_cast<uint64_t>(d.Q) * es, 32, 32, what, yswz);
         if (st != MILO_OK) return st;
     }
-    const int grid = p.two ? 2 * std::min(p.tiles, slots) : p.split > 1 ? p.tiles * p.split : std::min(p.tiles, sms);
+    const int used = p.split > 1 ? p.tiles : std::min(p.tiles, slots);       // CTAs, pairs or clusters at work
+    const int grid = used * (p.two ? 2 : p.split);
+    const double slice = slice_cycles(p.bn, p.two);
+    const auto cycles = [&](int i) { return tile_cycles(p.prob[i].kblocks, slice, p.bn, p.bufs); };
+    p.rounds = p.prob[0].tiles / used;
+    p.extra = p.prob[0].tiles % used;
+    p.fill = n > 1 ? static_cast<int>(fill_tiles(cycles(0), cycles(1))) : 0;
     cudaError_t e;
     if (swap) e = launch_dense_tc<true, false, false>(p, grid, smem, s);
     else if (p.two) e = wide ? launch_dense_tc<false, true, true>(p, grid, smem, s) : launch_dense_tc<false, true, false>(p, grid, smem, s);
