@@ -39,9 +39,10 @@
 //     waits for its copies and products and frees TMEM before it leaves.
 //
 // Measured (B200, device time): 8192 x 14336 x 4096 bf16 with bias and gelu_tanh
-// 613 us = 1570 TFLOP/s, 0.96 of the cuBLAS burst rate measured on the same
-// GPUs (single CTAs 690 us: the operands' way from L2); dx and dW of 8192 x
-// 4096 x 4096 about 370 us together.  Small products are bound by latency:
+// 613 to 628 us = 1530 to 1570 TFLOP/s, 0.93 to 0.96 of the cuBLAS burst rate
+// measured on the same GPUs (single CTAs 690 us: the operands' way from L2); dx
+// and dW of 8192 x 4096 x 4096 about 370 us together (385 with their tiles dealt
+// round without regard to length).  Small products are bound by latency:
 // 64 x 2816 x 2048 fp16 8.6 us and 4999 x 64 x 2048 9.8 us, of which the first
 // loads take about 1.6 us, the cluster's exchange 1.5 and the launch 2.
 #include <cuda.h>
