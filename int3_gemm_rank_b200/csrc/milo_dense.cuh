@@ -33,9 +33,14 @@ struct DenseGemm {
 // relative error below 2^-21 + 2^-23 |v|, times v (1 - v / ...) <= 0.3 in the
 // result, so within 2^-20 (|z| + 1) of the function and far below the half
 // step of a 16-bit result.
+__device__ __forceinline__ float exp_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896f));
+    return r;
+}
 __device__ __forceinline__ float sigmoid_fast(float v) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-v)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_fast(-v)));
     return r;
 }
 
@@ -63,7 +68,7 @@ __device__ __forceinline__ float act_slope(float z) {
         const float g = sigmoid_fast(z);
         return g * fmaf(z, 1.0f - g, 1.0f);
     } else if constexpr (ACT == MILO_ACT_GELU) {
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * exp_fast(-0.5f * z * z) * 0.39894228040143268f;
     } else if constexpr (ACT == MILO_ACT_GELU_TANH) {
         // past |z| = 16 the slope is 0 or 1 to the last bit, and z^2 may overflow
         const float c = fminf(fmaxf(z, -16.0f), 16.0f);
