@@ -70,9 +70,18 @@ __device__ __forceinline__ void dz_load(const void* p, size_t row, int N, int n0
 // shared memory in lane order.  Bound by memory (dy and z read, dz written
 // once); many small blocks carry it: with two or four rows of a thread in
 // flight the registers cost more warps than the loads gain (8192 x 4096 bf16,
-// silu, sums alone: 31 us with one, 37 with two, 57 with four).
+// silu, sums alone: 28 us with one, 37 with two, 57 with four).
+// Blocks an SM should hold at the least, 0: as the compiler likes.  Sums alone,
+// 8192 x 8192, 16-bit dy: silu 49 us with seven, 56 without; gelu 102 with one
+// (so, as many registers as its loads like) and 91 without; no activation 26
+// with one and 29 without; at width 8191 silu 75 with one and 69 without.
+template <int DYT, bool VEC, int ACT>
+constexpr int dz_blocks() {
+    if (ACT == MILO_ACT_NONE || (ACT == MILO_ACT_RELU && !VEC)) return 1;
+    return ACT == MILO_ACT_SILU && VEC && DYT != MILO_F32 ? 7 : 0;
+}
 template <int DYT, int ZT, bool VEC, int ACT>
-__global__ void __launch_bounds__(kDzThreads) dense_dz_kernel(const DzParams p) {
+__global__ void __launch_bounds__(kDzThreads, dz_blocks<DYT, VEC, ACT>()) dense_dz_kernel(const DzParams p) {
     __shared__ float red[8][kDzCols];
     grid_dep_launch();
     grid_dep_wait();
@@ -211,7 +220,9 @@ static DenseWs dense_ws(int M, int N) {
     DenseWs w;
     w.ldz = static_cast<int>(round_up(N, 64));
     // rows of a block: 64, fewer while the blocks do not fill the SMs four deep --
-    // but up to 64 rows in one, whose column sums then need no second kernel
+    // but up to 64 rows in one, whose column sums then need no second kernel (128
+    // rows: 8192 x 8192 bf16 without an activation, sums alone, 26 us against 29,
+    // but with gelu 99 against 92, and 8192 x 4096 with silu 32 against 28)
     w.rows = 64;
     const long long col_blocks = (N + kDzCols - 1) / kDzCols;
     while (M > 64 && w.rows > 8 && (M + w.rows - 1) / w.rows * col_blocks < 4 * 148) w.rows /= 2;

@@ -39,7 +39,7 @@
 //     waits for its copies and products and frees TMEM before it leaves.
 //
 // Measured (B200, device time): 8192 x 14336 x 4096 bf16 with bias and gelu_tanh
-// 613 to 628 us = 1530 to 1570 TFLOP/s, 0.93 to 0.96 of the cuBLAS burst rate
+// 610 to 620 us = 1550 to 1580 TFLOP/s, 0.95 to 0.96 of the cuBLAS burst rate
 // measured on the same GPUs (single CTAs 690 us: the operands' way from L2); dx
 // and dW of 8192 x 4096 x 4096 about 370 us together (385 with their tiles dealt
 // round without regard to length).  Small products are bound by latency:
