@@ -572,6 +572,14 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         // (a pair's first CTA sees both CTAs' copies)
         for (int s = 0; s < p.stages && (!TWO || cta == 0); ++s)
             if (((filled >> s) & 1u) && !warp_wait(&full[s], (fph >> s) & 1u)) fail = true;
+        // Nor may a commit's arrival: the products' commits reach the barriers of
+        // both CTAs of a pair on their own, ordered by no cluster barrier, so each
+        // CTA waits for those on its own barriers -- the stages it filled last here,
+        // afull in the epilogue, done_bar here for the second CTA and in the MMA
+        // warp for the first.
+        for (int s = 0; s < p.stages && !fail; ++s)
+            if (((filled >> s) & 1u) && !warp_wait(&empty[s], (fph >> s) & 1u)) fail = true;
+        if (TWO && cta == 1 && !warp_wait(done_bar, 0)) fail = true;
         if (fail) st_bits |= MILO_DEV_TIMEOUT;
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
@@ -751,7 +759,8 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
     }
 
     if constexpr (TWO) {
-        // neither CTA leaves while the other's copies, products or arrivals reach it
+        // neither CTA leaves while the other's copies, products or remote arrivals reach
+        // it (the commits' arrivals have been waited for above, each by its own CTA)
         __syncwarp();
         cluster_arrive();
         cluster_wait();
