@@ -84,6 +84,9 @@ __device__ __forceinline__ uint32_t row_window(uintptr_t a, uint32_t len, uintpt
         };
         copy(a, a + len < lo ? a + len : lo);
         copy(a > hi ? a : hi, a + len);
+        // a later bulk copy to this place of the ring must not be overtaken by these
+        // stores (two pieces of a tensor at most have any)
+        if (lo > base || hi < a + len) fence_proxy_async_smem();
         return static_cast<uint32_t>(hi - lo);
     }
 }

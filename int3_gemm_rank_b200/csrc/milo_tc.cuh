@@ -178,11 +178,6 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_addr, uint64_t a_desc, uint
         ::"r"(d_addr), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Generic-proxy writes to shared memory made visible to the tensor core (async proxy).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 __device__ __forceinline__ void named_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }

@@ -40,3 +40,31 @@ def test_pairs_of_ctas_end_with_nothing_under_way(milo):
     torch.cuda.synchronize()
     assert int(st.item()) == 0
     assert all(torch.equal(a, b) for a, b in got)
+
+
+@pytest.mark.parametrize("H", [63, 331, 2051])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_rows_at_both_ends_of_a_tensor_off_16_bytes(milo, H, dt):
+    """Tensors whose first and last bytes lie inside a 16-byte piece: the rows
+    there come in part element by element, into places of the ring that bulk
+    copies fill before and after.  Without weights every element is a copy."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(22)
+    T, k = 9001, 2
+    # both ends of the expert rows among the first items of a warp
+    ends = torch.tensor([0, T * k - 1], device="cuda")
+    perm = torch.cat([ends, 1 + torch.randperm(T * k - 2, generator=gen, device="cuda")]).int()
+    route = {"ids": torch.zeros((T, k), dtype=torch.int32, device="cuda"), "inv_perm": perm}
+
+    def off(rows):                                 # rows at an odd element of a buffer
+        return torch.randn(rows * H + 1, generator=gen, device="cuda").to(dt)[1:].view(rows, H)
+
+    x, ys = off(T), off(T * k)
+    p = perm.long()
+    st = milo.new_status()
+    for _ in range(3):
+        xs = milo.milo_dispatch(x, route, dev_status=st)
+        assert torch.equal(xs[p], x.repeat_interleave(k, 0))
+        y = milo.milo_combine(ys, route, dev_status=st)
+        assert torch.equal(y, (ys[p[0::2]].float() + ys[p[1::2]].float()).to(dt))
+    assert int(st.item()) == 0
