@@ -381,9 +381,9 @@ MILO_API milo_status milo_combine_backward(const void* dy, milo_dtype dy_dt, int
  *   flags     0 or MILO_ROUTE_RENORM, as given to milo_route
  *   dlogits   [T, E] in dl_dt (F16, BF16 or F32), every element written
  * Limits as milo_route.  Errors: INVALID_ARG (T < 0, unknown flag or dtype,
- * NULL pointers), UNSUPPORTED_SHAPE.  Device: BAD_EXPERT_ID (an id outside
- * [0, E): that pick contributes nothing), NONFINITE (NaN/Inf logits; NaN
- * counts as -inf), FP16_RANGE.  dev_status may be NULL.  Stream-ordered.
+ * NULL or misaligned pointers), UNSUPPORTED_SHAPE.  Device: BAD_EXPERT_ID (an
+ * id outside [0, E): that pick contributes nothing), NONFINITE (NaN/Inf logits;
+ * NaN counts as -inf), FP16_RANGE.  dev_status may be NULL.  Stream-ordered.
  */
 MILO_API milo_status milo_route_backward(const uint16_t* logits, const int32_t* topk_ids, const float* topk_w,
                                          const float* dw, int32_t T, int32_t E, int32_t k, uint32_t flags,

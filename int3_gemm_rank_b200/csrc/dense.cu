@@ -248,8 +248,10 @@ extern "C" milo_status milo_dense_linear(const void* x, const void* W, milo_dtyp
     if (!x || !W || !y) return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear: NULL pointer");
     if (!aligned(x, 16) || !aligned(W, 16))
         return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear: x and W must be 16-byte aligned");
-    if (!aligned(y, elem(y_dt)) || !aligned(residual, elem(y_dt)) || !aligned(bias, 2) || !aligned(z, 2))
-        return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear: bias, residual, y and z must be aligned to their elements");
+    if (!aligned(y, elem(y_dt)) || !aligned(residual, elem(y_dt)) || !aligned(bias, 2) || !aligned(z, 2) ||
+        !aligned(dev_status, 4))
+        return fail(MILO_ERR_INVALID_ARG,
+                    "milo_dense_linear: bias, residual, y, z and dev_status must be aligned to their elements");
     const DenseGemm g = {x, W, K, K, 0, 0, M, N, K, dt == MILO_BF16, bias, residual, act, y, y_dt, z, dev_status};
     return launch_dense_gemm(g, "milo_dense_linear", static_cast<cudaStream_t>(stream));
 }
@@ -283,8 +285,9 @@ extern "C" milo_status milo_dense_linear_backward(const void* dy, milo_dtype dy_
         return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear_backward: NULL pointer");
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(dx, 16) || !aligned(dW, 16))
         return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear_backward: x, W, dx and dW must be 16-byte aligned");
-    if (!aligned(dy, elem(dy_dt)) || !aligned(z, 2) || !aligned(db, 2))
-        return fail(MILO_ERR_INVALID_ARG, "milo_dense_linear_backward: dy, z and db must be aligned to their elements");
+    if (!aligned(dy, elem(dy_dt)) || !aligned(z, 2) || !aligned(db, 2) || !aligned(dev_status, 4))
+        return fail(MILO_ERR_INVALID_ARG,
+                    "milo_dense_linear_backward: dy, z, db and dev_status must be aligned to their elements");
     if (!aligned(ws, 256)) return fail(MILO_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     const DenseWs w = dense_ws(M, N);
     if (ws_bytes < w.total) return fail(MILO_ERR_WORKSPACE, "milo_dense_linear_backward: workspace too small");

@@ -120,10 +120,16 @@ static void exchange_index(ExchangeParams& p) {
     p.wide = static_cast<long long>(p.T) * p.nv >= (1LL << 31);
 }
 
-static milo_status check_rows(const char* what, std::initializer_list<std::pair<const void*, milo_dtype>> rows) {
+// Addresses: rows at their elements, indices, weights and status at 32-bit words.
+static milo_status check_addresses(const char* what, std::initializer_list<std::pair<const void*, milo_dtype>> rows,
+                                   std::initializer_list<const void*> words) {
     for (const auto& r : rows)
         if (r.first && !aligned(r.first, dtype_size(r.second)))
             return fail(MILO_ERR_INVALID_ARG, std::string(what) + ": rows must be aligned to their elements");
+    for (const void* q : words)
+        if (!aligned(q, 4))
+            return fail(MILO_ERR_INVALID_ARG,
+                        std::string(what) + ": inv_perm, w, dw and dev_status must be aligned to 4 bytes");
     return MILO_OK;
 }
 
@@ -139,7 +145,7 @@ extern "C" milo_status milo_dispatch(const void* x, milo_dtype x_dt, int32_t T, 
     if (s != MILO_OK) return s;
     if (T == 0) return MILO_OK;
     if (!x || !xs || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_dispatch: NULL pointer");
-    if ((s = check_rows("milo_dispatch", {{x, x_dt}, {xs, xs_dt}})) != MILO_OK) return s;
+    if ((s = check_addresses("milo_dispatch", {{x, x_dt}, {xs, xs_dt}}, {inv_perm, w, dev_status})) != MILO_OK) return s;
     const ExchangeTypes ty{x_dt, xs_dt, exchange_aligned(H, {x, xs})};
     ExchangeParams p = {x, nullptr, inv_perm, w, xs, nullptr, dev_status, T, k, H, 0, 0, 0, 0};
     exchange_index(p);
@@ -154,7 +160,8 @@ extern "C" milo_status milo_combine(const void* ys, milo_dtype ys_dt, int32_t T,
     if (s != MILO_OK) return s;
     if (T == 0) return MILO_OK;
     if (!ys || !y || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_combine: NULL pointer");
-    if ((s = check_rows("milo_combine", {{ys, ys_dt}, {y, y_dt}, {residual, y_dt}})) != MILO_OK) return s;
+    if ((s = check_addresses("milo_combine", {{ys, ys_dt}, {y, y_dt}, {residual, y_dt}}, {inv_perm, w, dev_status})) != MILO_OK)
+        return s;
     const ExchangeTypes ty{ys_dt, y_dt, exchange_aligned(H, {ys, y, residual})};
     ExchangeParams p = {ys, residual, inv_perm, w, y, nullptr, dev_status, T, k, H, 0, 0, 0, 0};
     exchange_index(p);
@@ -171,7 +178,8 @@ extern "C" milo_status milo_dispatch_backward(const void* dxs, milo_dtype dxs_dt
         return fail(MILO_ERR_INVALID_ARG, "milo_dispatch_backward: dw needs the call's w and x");
     if (T == 0) return MILO_OK;
     if (!dxs || !dx || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_dispatch_backward: NULL pointer");
-    if ((s = check_rows("milo_dispatch_backward", {{dxs, dxs_dt}, {dx, dx_dt}, {dw ? x : nullptr, dxs_dt}})) != MILO_OK)
+    if ((s = check_addresses("milo_dispatch_backward", {{dxs, dxs_dt}, {dx, dx_dt}, {dw ? x : nullptr, dxs_dt}},
+                             {inv_perm, w, dw, dev_status})) != MILO_OK)
         return s;
     const ExchangeTypes ty{dxs_dt, dx_dt, exchange_aligned(H, {dxs, dx, dw ? x : nullptr})};
     ExchangeParams p = {dxs, nullptr, inv_perm, w, dx, dw, dev_status, T, k, H, 0, 0, 0, 0};
@@ -193,7 +201,8 @@ extern "C" milo_status milo_combine_backward(const void* dy, milo_dtype dy_dt, i
         return fail(MILO_ERR_INVALID_ARG, "milo_combine_backward: dw needs the call's w and ys");
     if (T == 0) return MILO_OK;
     if (!dy || !dys || !inv_perm) return fail(MILO_ERR_INVALID_ARG, "milo_combine_backward: NULL pointer");
-    if ((s = check_rows("milo_combine_backward", {{dy, dy_dt}, {dys, dys_dt}, {dw ? ys : nullptr, dy_dt}})) != MILO_OK)
+    if ((s = check_addresses("milo_combine_backward", {{dy, dy_dt}, {dys, dys_dt}, {dw ? ys : nullptr, dy_dt}},
+                             {inv_perm, w, dw, dev_status})) != MILO_OK)
         return s;
     const ExchangeTypes ty{dy_dt, dys_dt, exchange_aligned(H, {dy, dys, dw ? ys : nullptr})};
     ExchangeParams p = {dy, nullptr, inv_perm, w, dys, dw, dev_status, T, k, H, 0, 0, 0, 0};

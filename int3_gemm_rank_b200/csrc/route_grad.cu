@@ -208,6 +208,9 @@ extern "C" milo_status milo_route_backward(const uint16_t* logits, const int32_t
         return fail(MILO_ERR_INVALID_ARG, "milo_route_backward: NULL pointer");
     if (!aligned(dlogits, dl_dt == MILO_F32 ? 4 : 2))
         return fail(MILO_ERR_INVALID_ARG, "milo_route_backward: dlogits must be aligned to its elements");
+    if ((!renorm && !aligned(logits, 2)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(dw, 4) || !aligned(dev_status, 4))
+        return fail(MILO_ERR_INVALID_ARG,
+                    "milo_route_backward: logits, topk_ids, topk_w, dw and dev_status must be aligned to their elements");
     const int vec = E % 8 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
     const RouteGradArgs a = {logits, topk_ids, topk_w, dw, T, E, k, renorm ? 1 : 0, vec, dlogits, dev_status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
