@@ -275,7 +275,8 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const float* bias) {
 // stores up to the `left` newest have to be out of `zbuf`, and without a residual
 // out of `buf`, before they are written.
 __device__ __forceinline__ void wide_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* buf, uint8_t* zbuf,
-                                           int left, const float* bias, int p0, int q0, int lane, int32_t& st) {
+                                           int left, const float* bias, int p0, int q0, int lane, int32_t& flags) {
+    int32_t st = 0;                          // counts where the lane's row exists: behind the last one it is act(bias)
     if (p.bias) add_bias(v, bias);
     if (p.z) {
         if (lane == 0) stores_read(left);
@@ -305,6 +306,7 @@ __device__ __forceinline__ void wide_chunk(const DenseTc& p, const DenseProb& d,
         }
         wide_put<DT>(&d.y_map, v, buf, p0, q0, lane, st);
     });
+    if (p0 + lane < d.P) flags |= st;
 }
 
 // Narrow form: the warp's block between staging rows (dense_pitch) and global
@@ -372,7 +374,8 @@ __device__ __forceinline__ void narrow_put(const DenseProb& d, void* g, const fl
 }
 
 __device__ __forceinline__ void narrow_chunk(const DenseTc& p, const DenseProb& d, float (&v)[32], uint8_t* stg,
-                                             const float* bias, int p0, int q0, int lane, int32_t& st) {
+                                             const float* bias, int p0, int q0, int lane, int32_t& flags) {
+    int32_t st = 0;                          // as in wide_chunk
     if (p.bias) add_bias(v, bias);
     if (p.z) {
         if (p.bf16) narrow_put<MILO_BF16>(d, p.z, v, stg, p0, q0, lane, st);
@@ -401,6 +404,7 @@ __device__ __forceinline__ void narrow_chunk(const DenseTc& p, const DenseProb& 
         }
         narrow_put<DT>(d, d.y, v, stg, p0, q0, lane, st);
     });
+    if (p0 + lane < d.P) flags |= st;
 }
 
 // Swapped form: the lane's row is feature p0 + lane, its N values tokens q0..:

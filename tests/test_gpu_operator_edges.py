@@ -68,3 +68,23 @@ def test_rows_at_both_ends_of_a_tensor_off_16_bytes(milo, H, dt):
         y = milo.milo_combine(ys, route, dev_status=st)
         assert torch.equal(y, (ys[p[0::2]].float() + ys[p[1::2]].float()).to(dt))
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("M,N", [(17, 64), (65, 64), (65, 63), (300, 64), (300, 66), (301, 63), (2600, 2312), (2601, 2312),
+                                 (2601, 2311), (20001, 120), (20001, 121)])
+def test_no_range_flag_from_a_bias_above_fp16(milo, M, N):
+    """bf16 operands, an fp16 output: a bias that fp16 does not hold, taken back
+    into range by the residual in every row there is, flags nothing -- the rows
+    that fill up a ragged block have the bias but no residual.  One row without
+    the residual does flag."""
+    x, W = torch.zeros((M, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((N, 64), dtype=torch.bfloat16, device="cuda")
+    b = torch.full((N,), 1e5, dtype=torch.bfloat16, device="cuda")
+    r = torch.full((M, N), -65000.0, dtype=torch.float16, device="cuda")
+    st = milo.new_status()
+    y = milo.milo_dense_linear(x, W, b, "none", r, dev_status=st)
+    want = torch.tensor(float(b[0]) + float(r[0, 0])).half().item()
+    assert bool((y == want).all()) and int(st.item()) == 0
+    r[M - 1] = 0.0
+    y = milo.milo_dense_linear(x, W, b, "none", r, dev_status=st)
+    assert bool(torch.isinf(y[M - 1]).all()) and bool((y[:M - 1] == want).all())
+    assert int(st.item()) == milo.MILO_DEV_FP16_RANGE
