@@ -525,11 +525,12 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         tma_load_2d(stg + buf * p.out_bytes, &p.r_map, bar, q0, p0);
     };
     float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + ew * kDtBias;
+    uint32_t filled = 0, fph = 0;                // producer: stages filled, their last phases
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
         int stage = 0;
-        uint32_t phase = 0, filled = 0, fph = 0;
+        uint32_t phase = 0;
         bool fail = false;
         const uint32_t tx = (TWO ? 2 : 1) * p.stage_bytes;
         const int bq = TWO ? p.bn / 2 : p.bn;        // B rows this CTA brings
@@ -576,14 +577,6 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
         // (a pair's first CTA sees both CTAs' copies)
         for (int s = 0; s < p.stages && (!TWO || cta == 0); ++s)
             if (((filled >> s) & 1u) && !warp_wait(&full[s], (fph >> s) & 1u)) fail = true;
-        // Nor may a commit's arrival: the products' commits reach the barriers of
-        // both CTAs of a pair on their own, ordered by no cluster barrier, so each
-        // CTA waits for those on its own barriers -- the stages it filled last here,
-        // afull in the epilogue, done_bar here for the second CTA and in the MMA
-        // warp for the first.
-        for (int s = 0; s < p.stages && !fail; ++s)
-            if (((filled >> s) & 1u) && !warp_wait(&empty[s], (fph >> s) & 1u)) fail = true;
-        if (TWO && cta == 1 && !warp_wait(done_bar, 0)) fail = true;
         if (fail) st_bits |= MILO_DEV_TIMEOUT;
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
@@ -764,7 +757,7 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
 
     if constexpr (TWO) {
         // neither CTA leaves while the other's copies, products or remote arrivals reach
-        // it (the commits' arrivals have been waited for above, each by its own CTA)
+        // it (the commits' arrivals, which no barrier of the cluster orders: below)
         __syncwarp();
         cluster_arrive();
         cluster_wait();
@@ -826,6 +819,18 @@ __global__ void __launch_bounds__(kDtThreads) dense_tc_kernel(const __grid_const
                 }
             }
         }
+    }
+    // Nor does a CTA leave while a commit's arrival is on its way to its barriers (a
+    // pair's commits arrive in both CTAs): those on the stages filled last and the
+    // second CTA's done_bar are waited for here, beside the epilogue's last blocks (in
+    // the producer's branch above, ahead of a split's barriers, this took 0.8 us of
+    // 9); afull's were in the epilogue, done_bar's in the MMA warp.
+    if (warp == 0) {
+        bool ok = true;
+        for (int s = 0; s < p.stages && ok; ++s)
+            if ((filled >> s) & 1u) ok = warp_wait(&empty[s], (fph >> s) & 1u);
+        if (TWO && cta == 1 && !warp_wait(done_bar, 0)) ok = false;
+        if (!ok) st_bits |= MILO_DEV_TIMEOUT;
     }
     // the stores have left shared memory and reached the outputs
     if (WIDE && warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
