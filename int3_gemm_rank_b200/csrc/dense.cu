@@ -72,9 +72,10 @@ __device__ __forceinline__ void dz_load(const void* p, size_t row, int N, int n0
 // flight the registers cost more warps than the loads gain (8192 x 4096 bf16,
 // silu, sums alone: 28 us with one, 37 with two, 57 with four).
 // Blocks an SM should hold at the least, 0: as the compiler likes.  Sums alone,
-// 8192 x 8192, 16-bit dy: silu 49 us with seven, 56 without; gelu 102 with one
-// (so, as many registers as its loads like) and 91 without; no activation 26
-// with one and 29 without; at width 8191 silu 75 with one and 69 without.
+// 8192 x 8192, 16-bit dy: silu 49 us with seven, 56 without; gelu 76 with one
+// (so, as many registers as its loads like), 72 with seven and 69 without; no
+// activation 26 with one and 29 without; at width 8191 silu 75 with one and 69
+// without.
 template <int DYT, bool VEC, int ACT>
 constexpr int dz_blocks() {
     if (ACT == MILO_ACT_NONE || (ACT == MILO_ACT_RELU && !VEC)) return 1;

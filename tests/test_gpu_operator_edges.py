@@ -1,6 +1,8 @@
 """Edges of the 16-bit operators on the GPU that their main suites do not reach:
 what a kernel leaves under way when it ends, flags of rows that do not exist,
 far tails of the activations, calls beside the library's other kernels."""
+import math
+
 import numpy as np
 import pytest
 
@@ -88,3 +90,67 @@ def test_no_range_flag_from_a_bias_above_fp16(milo, M, N):
     y = milo.milo_dense_linear(x, W, b, "none", r, dev_status=st)
     assert bool(torch.isinf(y[M - 1]).all()) and bool((y[:M - 1] == want).all())
     assert int(st.item()) == milo.MILO_DEV_FP16_RANGE
+
+
+@pytest.mark.parametrize("M", [8, 200])
+@pytest.mark.parametrize("dt,out", [("bf16", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+def test_gelu_far_below_zero_relative_to_its_value(milo, M, dt, out):
+    """gelu(z) = z erfc(-z / sqrt 2) / 2 and its slope from -3 down to where fp32 still
+    holds them as normal numbers, relative to their values.  In fp32 the argument
+    is off by 2^-23 (constant and product), which erfc multiplies by at most
+    z^2 + 1; erfcf is within 4 steps of 2^-23, the two products 2^-24 each: (z^2 +
+    6) 2^-23.  In the slope Phi + z phi, |z phi| >= 9 Phi here; exp is off by
+    z^2 / 2 times 2^-23 from its argument, 2^-21 of its own with the products."""
+    v = np.resize(-np.linspace(3.0, 12.0, 64), (M, 64)) * (1.0 + np.arange(M)[:, None] * 1e-4)
+    x = torch.from_numpy(v).to(torch.bfloat16 if dt == "bf16" else torch.float16).cuda()
+    W = torch.eye(64, dtype=x.dtype, device="cuda")
+    z = n64(x)
+    Phi = 0.5 * np.vectorize(math.erfc)(-z / math.sqrt(2.0))
+    zphi = z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    y = milo.milo_dense_linear(x, W, None, "gelu", out_dtype={"bf16": torch.bfloat16, "f32": torch.float32}[out])
+    rel = (z * z + 6.0) * 2.0 ** -23
+    check(y, z * Phi, np.abs(z * Phi) * (rel + R.U[out] * (1.0 + rel)), "y")
+    if dt == "bf16" and out == "bf16":
+        dy = torch.ones((M, 64), dtype=torch.bfloat16, device="cuda")
+        s = Phi + zphi
+        err = rel * Phi + (z * z * 2.0 ** -24 + 2.0 ** -21) * np.abs(zphi)
+        dx = milo.milo_dense_linear_backward(dy, x, W, "gelu", x, need=("dx",))["dx"]
+        check(dx, s, err + R.U["bf16"] * (np.abs(s) + err), "dx")
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_gelu_over_its_range_and_at_its_ends(milo, M):
+    """Every few bf16 values of [-13, 13]: gelu(z) = max(z, 0) - |z| Phi(-|z|) and the
+    slope's Phi and z phi.  Phi(-a) is within (a^2 + 9) 2^-23 of its value, relative
+    to it: the exponential's argument a^2 / 2 times 2^-23, the exponential 2^-22.5,
+    the reciprocal 2^-23 and its argument 2^-24, each at most 3.2 times (the slope of ln
+    r over ln t, largest at 0), the fit and the Horner steps 2^-23, two products.
+    Infinities give the limits, NaN stays NaN."""
+    zs = torch.arange(0x3A00, 0x4150, 8 if M == 8 else 1, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)   # 4.9e-4 to 13
+    zs = torch.cat([zs, -zs])
+    v = zs.repeat(-(-M * 64 // len(zs)))[:M * 64]
+    x = v.view(M, 64).cuda()
+    W = torch.eye(64, dtype=x.dtype, device="cuda")
+    z = n64(x)
+    a = np.abs(z)
+    q = 0.5 * np.vectorize(math.erfc)(a / math.sqrt(2.0))
+    eq = q * (a * a + 9.0) * 2.0 ** -23 + 2.0 ** -126          # below the normal range flushed
+    y = np.maximum(z, 0.0) - a * q
+    got = milo.milo_dense_linear(x, W, None, "gelu", out_dtype=torch.float32)
+    check(got, y, a * eq + 2.0 ** -24 * np.abs(y) + 2.0 ** -149, "y")
+    dy = torch.ones_like(x)
+    s = np.where(z > 0, 1.0 - q, q) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    # e (r - a / sqrt(2 pi)): as q, and the same for a phi; the 1 - of the upper half
+    es = eq + a * np.exp(-0.5 * z * z) * 0.4 * (a * a + 9.0) * 2.0 ** -23 + 2.0 ** -24 + a * 2.0 ** -126
+    dx = milo.milo_dense_linear_backward(dy, x, W, "gelu", x, need=("dx",))["dx"]
+    check(dx, s, es + R.U["bf16"] * (np.abs(s) + es), "dx")
+
+    ends = torch.tensor([math.inf, -math.inf, math.nan, 0.0, -0.0, 1e30, -1e30, 3e38], dtype=torch.bfloat16)
+    b = ends.repeat(8).cuda()
+    zero = torch.zeros((M, 64), dtype=torch.bfloat16, device="cuda")
+    y = milo.milo_dense_linear(zero, W, b, "gelu", out_dtype=torch.float32)
+    want = torch.tensor([math.inf, 0.0, math.nan, 0.0, 0.0, float(ends[5]), 0.0, float(ends[7])]).repeat(M, 8).cuda()
+    assert torch.equal(torch.nan_to_num(y, nan=7.0, posinf=8.0), torch.nan_to_num(want, nan=7.0, posinf=8.0))
+    db = milo.milo_dense_linear_backward(dy[:1], x[:1], W, "gelu", b.view(1, 64), need=("db",))["db"]
+    want = torch.tensor([1.0, 0.0, math.nan, 0.5, 0.5, 1.0, 0.0, 1.0]).repeat(8).cuda()
+    assert torch.equal(torch.nan_to_num(db.float(), nan=7.0), torch.nan_to_num(want, nan=7.0))
