@@ -1108,8 +1108,8 @@ static milo_status launch_dense(const DenseGemm* gs, int n, bool swap, const cha
     // that run side by side never ask for more than the SM's 512 columns: an
     // allocation that waited while its cluster's other CTAs hold theirs could
     // wait for ever on a cluster of another stream in the same position.
-    const int smem = std::max(p.off_bar + 512 + 1024,
-                              static_cast<int>(p.tmem_cols) * ((kDtSmemMax + 1024) / 512));
+    const int smem = std::max({p.off_bar + 512 + 1024, kTmemLeastShared,
+                               static_cast<int>(p.tmem_cols) * ((kDtSmemMax + 1024) / 512)});
     p.bias = g.bias;
     p.residual = g.residual;
     p.z = g.z;

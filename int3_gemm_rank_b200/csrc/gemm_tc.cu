@@ -73,7 +73,9 @@ constexpr int kTcDBufs = (512 - 128 - kTcTok) / kTcTok;   // TMEM accumulators D
 constexpr int kTcNumBars = 2 * kTcStages + 2 * 2 + 2 * kTcDBufs + 1 + 4 + 1;   // + done, xfull[2], xempty[2], zempty
 constexpr int kTcTab = kTcBar + 8 * kTcNumBars + 16;
 constexpr int kTcSmemUsed = kTcTab + 3 * (MILO_MAX_EXPERTS + 1) * 4;
-constexpr int kTcSmemBytes = kTcSmemUsed + 1024;        // slack to align the base to 1024 B
+// slack to align the base to 1024 B; all TMEM columns are this CTA's, so no other
+// CTA with columns may fit beside it (see milo_tc.cuh)
+constexpr int kTcSmemBytes = kTcSmemUsed + 1024 > kTmemAloneShared ? kTcSmemUsed + 1024 : kTmemAloneShared;
 constexpr int kTcFoldWarps = 8;             // two per TMEM lane quarter, kTcHalf routed rows each
 constexpr int kTcThreads = 32 * (2 + 4 + kTcFoldWarps);   // producer, MMA, extraction, fold
 constexpr uint32_t kTcTmemCols = 512;       // A: 2 x 64 columns, D_g: kTcDBufs x kTcTok, Z: kTcTok
@@ -86,6 +88,7 @@ static_assert(kTcDCol % 32 == 0 && kTcTok % 32 == 0 && kTcZCol % 32 == 0, "accum
 static_assert(kTcOffUB + 64 * MILO_MAX_RANK * 2 <= kTcStage, "compensator stage: U rows");
 static_assert(kTcOffUA + kTcRows * MILO_MAX_RANK * 2 <= kTcStage, "compensator stage: plain U rows");
 static_assert(kTcSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kTcSmemBytes + kTmemLeastShared + 2 * kCtaReservedBytes > kSmSharedBytes, "a second CTA with TMEM columns fits");
 static_assert(kTcZCol + kTcTok <= static_cast<int>(kTcTmemCols), "TMEM columns");
 
 struct TcItem {

@@ -12,6 +12,16 @@
 
 namespace milo {
 
+// Tensor memory beside other kernels.  An allocation waits while the SM's 512
+// columns are taken, without a limit, so no CTA that needs columns may land beside
+// one that holds too many: a CTA asks for at least its columns' share of the SM's
+// shared memory (dense_tc.cu), or takes all columns and so much shared memory that
+// no other of this library's TMEM users fits (gemm_tc.cu).
+constexpr int kSmSharedBytes = 228 * 1024;      // of an SM; a CTA takes 1 KB beside what it asks for
+constexpr int kCtaReservedBytes = 1024;
+constexpr int kTmemLeastShared = 37 * 1024;     // what every CTA with TMEM columns asks for at the least
+constexpr int kTmemAloneShared = kSmSharedBytes - 2 * kCtaReservedBytes - kTmemLeastShared + 1024;
+
 // TMEM address: lane in bits 31..16, column in bits 15..0.
 __device__ __forceinline__ uint32_t tmem_addr(uint32_t base, int lane, int col) {
     return base + (static_cast<uint32_t>(lane) << 16) + static_cast<uint32_t>(col);

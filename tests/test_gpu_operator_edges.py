@@ -154,3 +154,44 @@ def test_gelu_over_its_range_and_at_its_ends(milo, M):
     db = milo.milo_dense_linear_backward(dy[:1], x[:1], W, "gelu", b.view(1, 64), need=("db",))["db"]
     want = torch.tensor([1.0, 0.0, math.nan, 0.5, 0.5, 1.0, 0.0, 1.0]).repeat(8).cuda()
     assert torch.equal(torch.nan_to_num(db.float(), nan=7.0), torch.nan_to_num(want, nan=7.0))
+
+
+def test_small_products_beside_the_grouped_gemm(milo):
+    """The grouped int3 GEMM on the tensor cores (all TMEM columns of its SMs) on
+    two streams, small dense products (tokens as columns, split over clusters)
+    and pairs of CTAs on two others: each as alone, no wait runs out."""
+    import workloads as wl
+    from parity_util import f16_dev
+    rng = np.random.default_rng(23)
+    P = [wl.make_projection("t_mix", "w", e, 512, 1024, rk) for e, rk in enumerate((16, 0, 32, 8))]
+    lin = milo.GroupedLinear([milo.QWeight.quantize(f16_dev(p.W), f16_dev(p.U) if p.rank else None,
+                                                    f16_dev(p.V) if p.rank else None) for p in P])
+    T, k = 3000, 2
+    x, logits = rand(rng, (T, 1024), "bf16"), rand(rng, (T, 4), "f16")
+    st = milo.new_status()
+    r = milo.milo_route(logits, k, True, dev_status=st)
+    dense = [(rand(rng, (M, K), "bf16"), rand(rng, (N, K), "bf16", K ** -0.5))
+             for M, N, K in ((20, 512, 4096), (64, 2816, 2048), (300, 64, 2048), (2600, 2312, 264))]
+    milo.milo_set_gemm_path("tc")
+    try:
+        want = lin(x, r["offsets"], r["perm"], k=k, dev_status=st)
+        ys = [milo.milo_dense_linear(a, b, dev_status=st) for a, b in dense]
+        # a workspace of its own for each of the two streams
+        linears = [lin, milo.GroupedLinear(lin.weights)]
+        for g in linears:
+            g(x, r["offsets"], r["perm"], k=k)
+        streams = [torch.cuda.Stream() for _ in range(4)]
+        torch.cuda.synchronize()
+        got = []
+        for i in range(20):
+            for j in (0, 1):
+                with torch.cuda.stream(streams[j]):
+                    got.append((linears[j](x, r["offsets"], r["perm"], k=k, dev_status=st), want))
+            for j in (2, 3):
+                with torch.cuda.stream(streams[j]):
+                    for (a, b), y in zip(dense, ys):
+                        got.append((milo.milo_dense_linear(a, b, dev_status=st), y))
+        torch.cuda.synchronize()
+    finally:
+        milo.milo_set_gemm_path("auto")
+    assert int(st.item()) == 0 and all(torch.equal(a, b) for a, b in got)
