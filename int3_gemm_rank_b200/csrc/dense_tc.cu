@@ -65,7 +65,7 @@ constexpr int kDtAtom = kDtRows * kDtK * 2;  // bytes of an A stage
 constexpr int kDtBox = 64 * kDtK * 2;        // bytes of an MN-major box (64 rows x 64 c)
 constexpr int kDtEpiWarps = 8;               // two per TMEM lane quarter, every other block of columns each
 constexpr int kDtThreads = 32 * (2 + kDtEpiWarps);   // producer, MMA, epilogue
-constexpr int kDtMaxStages = 12;
+constexpr int kDtMaxStages = 12;             // below 31 (a lane each at the end)
 constexpr int kDtMaxSplit = 8;               // portable cluster size
 constexpr int kDtChunk = 32;                 // accumulator columns handled at a time
 constexpr int kDtOutBufs = 4;                // output buffers of an epilogue warp, at most
@@ -824,15 +824,15 @@ __global__ void __launch_bounds__(kDtThreads, SWAP ? 2 : 0) dense_tc_kernel(cons
     }
     // Nor does a CTA leave while a commit's arrival is on its way to its barriers (a
     // pair's commits arrive in both CTAs): those on the stages filled last and the
-    // second CTA's done_bar are waited for here, beside the epilogue's last blocks (in
-    // the producer's branch above, ahead of a split's barriers, this took 0.8 us of
-    // 9); afull's were in the epilogue, done_bar's in the MMA warp.
+    // second CTA's done_bar are waited for here, a lane each, beside the epilogue's
+    // last blocks (32 x 4096 x 4096 11.4 us; stage by stage 12.0, in the producer's branch
+    // above, ahead of a split's barriers, 12.7); afull's were in the epilogue,
+    // done_bar's in the MMA warp.
     if (warp == 0) {
         bool ok = true;
-        for (int s = 0; s < p.stages && ok; ++s)
-            if ((filled >> s) & 1u) ok = warp_wait(&empty[s], (fph >> s) & 1u);
-        if (TWO && cta == 1 && !warp_wait(done_bar, 0)) ok = false;
-        if (!ok) st_bits |= MILO_DEV_TIMEOUT;
+        if (lane < p.stages && ((filled >> lane) & 1u)) ok = mbar_wait(&empty[lane], (fph >> lane) & 1u);
+        if (TWO && cta == 1 && lane == 31) ok = mbar_wait(done_bar, 0);
+        if (!__all_sync(0xFFFFFFFFu, ok)) st_bits |= MILO_DEV_TIMEOUT;
     }
     // the stores have left shared memory and reached the outputs
     if (WIDE && warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
