@@ -409,7 +409,10 @@ MILO_API milo_status milo_route_backward(const uint16_t* logits, const int32_t* 
  * milo_dense_linear -- z = x W^T + bias;  y = act(z) + residual, in one kernel.
  *   bias      [N] in dt, or NULL
  *   residual  [M, N] in y_dt, or NULL; may be y's own buffer
- *   y         [M, N] in y_dt (F16, BF16 or F32), rounded once from fp32
+ *   y         [M, N] in y_dt (F16, BF16 or F32), rounded once from fp32; there an
+ *             activation is within (3 + |u|) 2^-21 of its value, relative to it, u
+ *             its exponential's argument (silu z, gelu z^2 / 2, gelu_tanh sqrt(8/pi)
+ *             (z + 0.044715 z^3)); values below 2^-119 may come out as 0
  *   z         NULL, or [M, N] in dt: the pre-activation, which
  *             milo_dense_linear_backward needs when there is an activation
  * x and W 16-byte aligned, the others aligned to their elements; y overlaps no

@@ -32,19 +32,21 @@
 //   - Outputs of whole 16-byte pieces leave by TMA, and a residual's blocks come
 //     by it, up to three ahead of the accumulators (2780 x 8424 x 72 with both: 47
 //     us, 99 with loads that a warp waits for).  Other widths go through a staging
-//     buffer by words or elements, eight loads under way (2780 x 8420 x 72: 69 us,
+//     buffer by words or elements, eight loads under way (2780 x 8420 x 72: 70 us,
 //     2780 x 8419 x 72: 96; one load at a time 268).  The two forms are kernels of
 //     their own: in one, the second's registers slowed the first by 3 to 15%.
 //   - Every wait is bounded: on a timeout the kernel flags MILO_DEV_TIMEOUT,
 //     waits for its copies and products and frees TMEM before it leaves.
 //
 // Measured (B200, device time): 8192 x 14336 x 4096 bf16 with bias and gelu_tanh
-// 610 to 620 us = 1550 to 1580 TFLOP/s, 0.95 to 0.96 of the cuBLAS burst rate
-// measured on the same GPUs (single CTAs 690 us: the operands' way from L2); dx
-// and dW of 8192 x 4096 x 4096 about 370 us together (385 with their tiles dealt
-// round without regard to length).  Small products are bound by latency:
-// 64 x 2816 x 2048 fp16 8.6 us and 4999 x 64 x 2048 9.8 us, of which the first
-// loads take about 1.6 us, the cluster's exchange 1.5 and the launch 2.
+// 612 to 633 us from GPU to GPU = 1520 to 1570 TFLOP/s, 0.93 to 0.96 of the cuBLAS
+// burst rate (single CTAs 690 us: the operands' way from L2); dx and dW of 8192 x
+// 4096 x 4096 370 to 388 us together (385 with their tiles dealt round without
+// regard to length, where 370 was).  Small products are bound by latency, not by
+// the tensor cores or memory (5% of the pipe, 10 to 13% of DRAM): 64 x 2816 x 2048
+// fp16 8.6 us and 4999 x 64 x 2048 9.4 to 10.0 us, of which the first loads take about
+// 1.6 us, the cluster's exchange 1.5 and the launch 2; the rest, barriers and output,
+// has not been told apart.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>

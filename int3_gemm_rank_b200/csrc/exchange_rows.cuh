@@ -24,9 +24,10 @@
 //
 // Measured (B200, device time, of the measured copy rate): combine 8192 x 2048,
 // k 6, bf16 with a residual 42.3 us (0.97; 54 with 8 warps a block, 48 with
-// 16); dispatch's gradient 8192 x 4096, k 2, bf16 31.6 us (0.97); combine's
-// gradient 5003 x 2048, k 6, fp16 47 us (0.82), and at width 2051 55 us
-// (0.70), where the one-element reads and stores bound it.  Threads that load
+// 16), at width 2047 48.5 us (0.85); dispatch's gradient 8192 x 4096, k 2, bf16 32.3
+// us (0.95), with router weights 43.1 us (0.95); combine's gradient 5003 x 2048, k
+// 6, fp16 47 us (0.82), and at width 2051 56 us (0.70), where the one-element
+// reads and stores bound it; dispatch 8192 x 2047, k 6, bf16 53 us (0.68).  Threads that load
 // the rows into registers reached 0.62 of the rate at best.
 #pragma once
 

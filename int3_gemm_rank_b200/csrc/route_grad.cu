@@ -27,10 +27,12 @@ struct RouteGradArgs {
 // (the Jacobian of a softmax q is q_i ([i = l] - q_l); the renormalised one
 // runs over the picked experts only).  L lanes share a token, eight experts
 // and every L-th pick each, so a warp takes 32 / L tokens and every reduction
-// has log2 L steps; the picks meet their experts in shared memory.  The
-// instructions, not the bytes, bound this: 65536 x 64, k 6, took 18.7 us with
-// a warp per token, 11 us with the picks compared in registers, and takes 9.5 us
-// (0.48 of the measured copy rate) so.
+// has log2 L steps; the picks meet their experts in shared memory.  What
+// bounds it is each warp's one chain of loads, shuffles and shared memory: 65536 x
+// 64, k 6, took 18.7 us with a warp per token, 11 us with the picks compared in
+// registers, and takes 9.5 us (0.48 of the measured copy rate) so, with 46% of the
+// issue slots taken and warps waiting for global (9.5 of 24 cycles an issue) and
+// shared memory (9.4).
 template <typename TO, int L, int KM, bool VEC>
 __global__ void __launch_bounds__(kRgThreads) route_grad_kernel(const RouteGradArgs p) {
     constexpr int kTok = kRgThreads / L, kRow = 8 * L + 4;

@@ -118,6 +118,26 @@ def test_gelu_far_below_zero_relative_to_its_value(milo, M, dt, out):
         check(dx, s, err + R.U["bf16"] * (np.abs(s) + err), "dx")
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [8, 200])
+def test_silu_and_gelu_tanh_relative_to_their_values(milo, act, M):
+    """fp32 outputs from deep in the negative tail up: with v the exponential's
+    argument, ex2 is within 2^-22.5, its argument (product and constant) 1.3 2^-24 |v|,
+    the sum 2^-24, the reciprocal 2^-23, the product 2^-24: below (5 + |v|) 2^-23 for
+    silu.  gelu_tanh's v has five roundings of 2^-24 at most of its own: (5 + 4 |v|)
+    2^-23."""
+    low = -80.0 if act == "silu" else -9.0
+    v = np.resize(np.linspace(low, 9.0, 251), (M, 64))
+    x = torch.from_numpy(v).bfloat16().cuda()
+    W = torch.eye(64, dtype=x.dtype, device="cuda")
+    z = n64(x)
+    u = z if act == "silu" else math.sqrt(8.0 / math.pi) * (z + 0.044715 * z ** 3)
+    want = z / (1.0 + np.exp(-u))
+    y = milo.milo_dense_linear(x, W, None, act, out_dtype=torch.float32)
+    rel = (5.0 + (1.0 if act == "silu" else 4.0) * np.abs(u)) * 2.0 ** -23
+    check(y, want, np.abs(want) * (rel + R.U["f32"] * (1.0 + rel)), act)
+
+
 @pytest.mark.parametrize("M", [8, 200])
 def test_gelu_over_its_range_and_at_its_ends(milo, M):
     """Every few bf16 values of [-13, 13]: gelu(z) = max(z, 0) - |z| Phi(-|z|) and the
