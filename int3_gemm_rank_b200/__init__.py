@@ -520,6 +520,8 @@ def milo_route_backward(route: dict, dw: torch.Tensor, renorm: bool, E: int, log
 # ---------------------------------------------------------------------------
 # token rows in expert order
 # ---------------------------------------------------------------------------
+# Here and below every gradient is a call of its own: nothing is recorded by
+# torch's autograd, also for inputs that require a gradient.
 
 # The current device and stream without building Device and Stream objects (a
 # Stream costs microseconds, as much as a small kernel).
