@@ -37,6 +37,7 @@
 
 #include "milo_exchange.cuh"
 #include "milo_host.h"
+#include "milo_tc.cuh"
 
 namespace milo {
 

@@ -295,12 +295,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // PTX: bulk copies (TMA engine, 1-D; no multicast anywhere in this library)
 // ---------------------------------------------------------------------------
 
-// This thread's generic-proxy writes to shared memory ordered before later
-// accesses of the async proxy (bulk copies, tensor core).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // L2 policy for data read once per launch (packed weights): evict first, so
 // that activations and partial sums stay resident.
 __device__ __forceinline__ uint64_t l2_evict_first() {

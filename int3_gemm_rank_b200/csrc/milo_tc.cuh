@@ -188,6 +188,12 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_addr, uint64_t a_desc, uint
         ::"r"(d_addr), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// This thread's generic-proxy writes to shared memory ordered before later
+// accesses of the async proxy (bulk copies, tensor core).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void named_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
